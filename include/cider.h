@@ -395,6 +395,148 @@ cider_status_t cider_stack_forward_dt(const void* x, int32_t dtype, int64_t M, i
                                       const cider_stack_layer_t* layers, void* workspace,
                                       int64_t workspace_bytes, void* y, void* stream);
 
+/* ---- Expert blocks ------------------------------------------------------------
+ * A mixture-of-experts block on quantized weights, and the boundary between
+ * two blocks. In the order of use, for T tokens with top_k experts each:
+ *   cider_norm_quant              residual -> codes of its norm
+ *   cider_moe_plan                the router's expert ids -> offsets, rows, slots
+ *   cider_w8a8_grouped_swiglu     codes[rows / top_k] x [gate; up] of each expert
+ *   cider_quant_act_dt            the expert rows' activations -> codes
+ *   cider_w8a8_grouped_gemm       x down projection of each expert
+ *   cider_norm_quant              the slots' weighted sum, added to the residual,
+ *                                 -> codes of the next block's norm
+ * None of them returns a size to the host, so the chain can be captured into a
+ * HIP graph and replayed for other routings of the same T.
+ */
+
+/* Most experts of one call, and most choices of one token (cider_norm_quant). */
+#define CIDER_MOE_MAX_EXPERTS 512
+#define CIDER_MOE_MAX_TOP_K 64
+
+/* Routing plan: the stable sort of P = T * top_k expert ids.
+ *   expert_ids : int32 [T, top_k]; an id outside [0, n_experts) belongs to no
+ *                expert (a padded token, an expert of another rank).
+ *   offsets    : int32 [n_experts + 1] (output): expert e has the sorted rows
+ *                offsets[e] .. offsets[e+1] - 1; offsets[0] = 0.
+ *   rows       : int32 [P] (output): rows[i] = the flat index t * top_k + j of
+ *                sorted row i, ascending within an expert; -1 for
+ *                i >= offsets[n_experts].
+ *   slots      : int32 [T, top_k] (output): the sorted row of each id, -1 for
+ *                an id of no expert.
+ * workspace: 16-byte aligned, at least cider_moe_plan_workspace_size(T, top_k,
+ * n_experts) bytes (0 up to 8192 ids, which take one launch; NULL then). Its
+ * contents are scratch; calls that share one must not overlap in time.
+ * T >= 0, top_k >= 1, T * top_k < 2^31, 1 <= n_experts <=
+ * CIDER_MOE_MAX_EXPERTS. T == 0 writes zero offsets. The result does not
+ * depend on timing (no order of atomics enters it). */
+int64_t cider_moe_plan_workspace_size(int64_t T, int32_t top_k, int32_t n_experts);
+cider_status_t cider_moe_plan(const int32_t* expert_ids, int64_t T, int32_t top_k, int32_t n_experts,
+                              int32_t* offsets, int32_t* rows, int32_t* slots, void* workspace,
+                              int64_t workspace_bytes, void* stream);
+
+/* W8A8 / W4A8 products grouped by expert. For every expert e and every row p
+ * in [offsets[e], offsets[e+1]):
+ *   y[p,n] = fp(((float)acc * x_scale[src]) * w_scale[e,n]),
+ *   acc = sum_k x_q[src,k] * w_q[e,n,k] (exact int32),
+ *   src = row_index ? row_index[p] / row_div : p.
+ * y is bit for bit what cider_w8a8_gemm_dt / cider_w4a8_gemm_dt computes for
+ * each expert's rows alone.
+ *   x_q       : int8 [x_rows, K], x_scale fp32 [x_rows].
+ *   w_q       : int8 [n_experts, N, K] (w_packed: uint8 [n_experts, N, K/2]),
+ *               w_scale fp32 [n_experts, N].
+ *   offsets   : int32 [n_experts + 1] on the DEVICE, ascending from 0 to at
+ *               most P (cider_moe_plan makes them). The group sizes may be
+ *               anything, zero included. Offsets that do not ascend within
+ *               0 .. P are clamped to it.
+ *   row_index : int32 [P] on the device or NULL; a row whose src is negative
+ *               or >= x_rows gives zeros. Without it x_rows must be >= P.
+ *   y         : fp16 or bf16 [P, N] (y_dtype); rows from offsets[n_experts]
+ *               on are left as they were.
+ * K a multiple of 16 (32 for packed weights), any N; one expert's weights
+ * must be below 2^31 bytes and, with row_index, so must x_q; 1 <= row_div;
+ * 1 <= n_experts <= CIDER_MOE_MAX_EXPERTS; P, x_rows < 2^31. (P, N) whose
+ * output tiles would take 2^31 GPU threads return CIDER_ERROR_INVALID_VALUE.
+ * P == 0 or N == 0 does nothing. Other errors as for cider_w8a8_gemm. */
+cider_status_t cider_w8a8_grouped_gemm(const int8_t* x_q, const float* x_scale, int64_t x_rows,
+                                       const int8_t* w_q, const float* w_scale, const int32_t* offsets,
+                                       const int32_t* row_index, int32_t row_div, int64_t P, int64_t N,
+                                       int64_t K, int32_t n_experts, void* y, int32_t y_dtype, void* stream);
+cider_status_t cider_w4a8_grouped_gemm(const int8_t* x_q, const float* x_scale, int64_t x_rows,
+                                       const uint8_t* w_packed, const float* w_scale, const int32_t* offsets,
+                                       const int32_t* row_index, int32_t row_div, int64_t P, int64_t N,
+                                       int64_t K, int32_t n_experts, void* y, int32_t y_dtype, void* stream);
+
+/* The same products with the gated activation fused into the store stage:
+ * weight rows 0 .. N/2 - 1 of an expert are its gate projection and rows
+ * N/2 .. N - 1 its up projection (N even), and
+ *   y[p,n] = fp(silu(v[p,n]) * v[p,N/2+n]), silu(g) = g / (1 + exp(-g)),
+ *   v = ((float)acc * x_scale[src]) * w_scale[e,.] as above, unrounded fp32,
+ * with y [P, N/2]. exp and the reciprocal are the GPU's fp32 instructions: the
+ * fp32 value is within (8 + |g|) * 2^-23 of the formula, relative, before it
+ * is rounded once to y's type (silu of g < -87 may be 0). All else as above.
+ * A dense gated MLP is the case n_experts = 1. */
+cider_status_t cider_w8a8_grouped_swiglu(const int8_t* x_q, const float* x_scale, int64_t x_rows,
+                                         const int8_t* w_q, const float* w_scale, const int32_t* offsets,
+                                         const int32_t* row_index, int32_t row_div, int64_t P, int64_t N,
+                                         int64_t K, int32_t n_experts, void* y, int32_t y_dtype, void* stream);
+cider_status_t cider_w4a8_grouped_swiglu(const int8_t* x_q, const float* x_scale, int64_t x_rows,
+                                         const uint8_t* w_packed, const float* w_scale, const int32_t* offsets,
+                                         const int32_t* row_index, int32_t row_div, int64_t P, int64_t N,
+                                         int64_t K, int32_t n_experts, void* y, int32_t y_dtype, void* stream);
+
+/* The boundary between two blocks in one launch: the finished block's output
+ * (a matrix, or the weighted sum of each token's expert rows) goes through an
+ * optional norm and gate into the residual, whose norm is quantized for the
+ * next block's linears. Per row m, all in fp32:
+ *   p = block[m], or sum_j weights[m,j] * block[slots[m,j]] (slots outside
+ *       [0, block_rows) add nothing)
+ *   p = p / sqrt(mean(p^2) + eps) * post_weight          (if post_weight)
+ *   h = fp(x[m] + alpha * gate[m / rows_per_gate] * p)   (x, gate: if given)
+ *   n = h / sqrt(mean(h^2) + eps) * norm_weight          (if norm_weight)
+ *   normed[m] = fp(n); x_q[m], x_scale[m] = n quantized by cider_quant_act's
+ *       rule (per row, or per group_size elements), n not rounded first.
+ * h is rounded to the 16-bit type before the second norm reads it, so that n
+ * belongs to the residual as stored. A row of zeros gives n = 0, scale 0.
+ *   x [M, K], block [M, K] (or [block_rows, K] with slots), h, normed [M, K],
+ *   post_weight, norm_weight [K], gate [ceil(M / rows_per_gate), K] (one row
+ *   for all with rows_per_gate 0): all fp16 or all bf16 (dtype);
+ *   slots int32 [M, top_k], weights fp32 [M, top_k] (both or neither).
+ * x or block must be given; without block h = x (post_weight, gate and slots
+ * must then be NULL), with block h must be given. h may be x itself (updated
+ * in place); no other buffers may overlap. x_q and x_scale go together; they
+ * and normed need norm_weight. alpha finite, eps positive and finite, 1 <=
+ * top_k <= CIDER_MOE_MAX_TOP_K with slots, M < 2^23, 1 <= K <= CIDER_MAX_K,
+ * K % group_size == 0. Values whose squares overflow fp32 are unspecified, as
+ * are non-finite ones. */
+typedef struct {
+  const void* x;
+  const void* block;
+  const int32_t* slots;
+  const float* weights;
+  const void* post_weight;
+  const void* gate;
+  const void* norm_weight;
+  void* h;
+  void* normed;
+  int8_t* x_q;
+  float* x_scale;
+  int64_t M, K;
+  int64_t block_rows;    /* rows of block, with slots */
+  int64_t rows_per_gate; /* 0: one gate row */
+  int32_t dtype;         /* a cider_dtype_t */
+  int32_t top_k;
+  int32_t group_size;
+  float alpha;
+  float eps;
+} cider_norm_quant_t;
+cider_status_t cider_norm_quant(const cider_norm_quant_t* args, void* stream);
+
+/* Codes back to rows, for consumers that are not quantized:
+ *   y[m,k] = fp((float)x_q[m,k] * x_scale[m] or x_scale[m, k / group_size]).
+ * Sizes and errors as for cider_quant_act; any K >= 1 with group_size 0. */
+cider_status_t cider_dequant_act(const int8_t* x_q, const float* x_scale, int64_t M, int64_t K,
+                                 int32_t group_size, void* y, int32_t y_dtype, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,122 @@
+"""The expert-block entry points reject bad arguments before touching HIP (no
+GPU needed), and their size queries."""
+import ctypes
+
+import pytest
+
+from w8a8_online_quantized_amd import cider
+
+P = ctypes.c_void_p(1 << 20)            # never dereferenced: the checks come first
+MIS = ctypes.c_void_p((1 << 20) + 8)
+NULL = None
+INV = cider.CIDER_ERROR_INVALID_VALUE
+MAX_E, MAX_K = 512, 133120
+
+
+@pytest.fixture(scope="module")
+def L():
+    return cider.lib()
+
+
+def test_plan_rejects(L):
+    def plan(ids=P, T=16, k=8, E=64, off=P, rows=P, slots=P, ws=NULL, wsb=0):
+        return L.cider_moe_plan(ids, T, k, E, off, rows, slots, ws, wsb, NULL)
+    assert plan(T=-1) == INV and plan(k=0) == INV and plan(E=0) == INV and plan(E=MAX_E + 1) == INV
+    assert plan(T=1 << 30, k=2) == INV                                      # T * top_k at 2^31
+    assert plan(ids=NULL) == INV and plan(off=NULL) == INV and plan(rows=NULL) == INV and plan(slots=NULL) == INV
+    assert plan(ids=MIS) == INV and plan(off=MIS) == INV and plan(rows=MIS) == INV and plan(slots=MIS) == INV
+    assert plan(T=0, off=NULL) == INV                                       # the offsets are written even then
+    need = L.cider_moe_plan_workspace_size(4096, 8, 64)
+    assert need > 0
+    assert plan(T=4096) == INV and plan(T=4096, ws=P, wsb=need - 1) == INV and plan(T=4096, ws=MIS, wsb=need) == INV
+
+
+def test_plan_workspace_query(L):
+    q = L.cider_moe_plan_workspace_size
+    assert q(0, 8, 64) == 0 and q(1024, 8, 64) == 0                         # 8192 ids: one launch
+    assert q(1025, 8, 64) == -(-8200 // 2048) * 64 * 4
+    assert q(1 << 20, 8, MAX_E) == 256 * MAX_E * 4                          # at most 256 blocks
+    assert q(-1, 8, 64) == -1 and q(1, 0, 64) == -1 and q(1, 1, 0) == -1 and q(1, 1, MAX_E + 1) == -1
+    assert q(1 << 31, 1, 4) == -1
+
+
+GROUPED = ["cider_w8a8_grouped_gemm", "cider_w4a8_grouped_gemm", "cider_w8a8_grouped_swiglu",
+           "cider_w4a8_grouped_swiglu"]
+
+
+@pytest.mark.parametrize("name", GROUPED)
+def test_grouped_rejects(L, name):
+    def call(x=P, sx=P, xr=64, w=P, sw=P, off=P, idx=NULL, div=1, rows=64, N=64, K=128, E=4, y=P, dt=0):
+        return getattr(L, name)(x, sx, xr, w, sw, off, idx, div, rows, N, K, E, y, dt, NULL)
+    i4 = "w4a8" in name
+    assert call(rows=-1) == INV and call(N=-2) == INV and call(K=0) == INV
+    assert call(K=136) == INV and call(K=MAX_K + 32) == INV
+    assert call(K=16) in ((INV,) if i4 else (0, cider.CIDER_ERROR_NOT_SUPPORTED))
+    assert call(E=0) == INV and call(E=MAX_E + 1) == INV and call(div=0) == INV and call(dt=2) == INV
+    assert call(xr=63) == INV and call(xr=-1) == INV                        # row p itself needs x_rows >= P
+    assert call(xr=1 << 31, idx=P) == INV and call(xr=1 << 24, idx=P) == INV   # codes at 2^31 bytes behind an index
+    assert call(N=1 << (25 if i4 else 24), K=128) == INV                    # one expert's weights at 2^31 bytes
+    if "swiglu" in name:
+        assert call(N=63) == INV
+    for bad in (dict(x=NULL), dict(sx=NULL), dict(w=NULL), dict(sw=NULL), dict(off=NULL), dict(y=NULL),
+                dict(x=MIS), dict(sx=MIS), dict(w=MIS), dict(sw=MIS), dict(off=MIS), dict(idx=MIS), dict(y=MIS)):
+        assert call(**bad) == INV, bad
+    assert call(rows=0, x=NULL, sx=NULL, w=NULL, sw=NULL, off=NULL, y=NULL, xr=0) == 0
+    assert call(N=0, x=NULL, sx=NULL, w=NULL, sw=NULL, off=NULL, y=NULL) == 0
+    # a grid of 2^31 threads
+    assert call(rows=(1 << 31) - 1, xr=(1 << 31) - 1, N=1 << 20, K=32, E=1) == INV
+
+
+def norm_args(**kw):
+    a = dict(x=1 << 20, block=1 << 21, norm_weight=1 << 22, h=1 << 23, x_q=1 << 24, x_scale=1 << 25, M=4, K=128,
+             dtype=0, alpha=1.0, eps=1e-6)
+    a.update(kw)
+    return cider.NormQuant(**a)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(M=-1), dict(M=1 << 23), dict(K=0), dict(K=MAX_K + 1), dict(K=100, group_size=64), dict(group_size=32),
+    dict(dtype=2), dict(eps=0.0), dict(eps=-1e-6), dict(eps=float("nan")), dict(eps=float("inf")),
+    dict(alpha=float("nan")), dict(alpha=float("inf")), dict(rows_per_gate=-1),
+    dict(slots=1 << 20), dict(weights=1 << 20),                             # one without the other
+    dict(slots=1 << 20, weights=1 << 20, top_k=0), dict(slots=1 << 20, weights=1 << 20, top_k=65),
+    dict(slots=1 << 20, weights=1 << 20, top_k=2, block_rows=-1),
+    dict(slots=1 << 20, weights=1 << 20, top_k=2, block_rows=1 << 31),
+    dict(x=None, block=None), dict(h=None),                                 # a block's residual has to go somewhere
+    dict(block=None, post_weight=1 << 20), dict(block=None, gate=1 << 20),
+    dict(block=None, slots=1 << 20, weights=1 << 20, top_k=1),
+    dict(x_q=None), dict(x_scale=None), dict(norm_weight=None), dict(norm_weight=None, x_q=None, x_scale=None,
+                                                                     normed=1 << 20),
+    dict(block=None, h=None, x_q=None, x_scale=None),                       # nothing to write
+    dict(x=(1 << 20) + 2), dict(block=(1 << 20) + 8), dict(h=(1 << 20) + 8), dict(x_q=(1 << 20) + 4),
+    dict(x_scale=(1 << 20) + 4), dict(norm_weight=(1 << 20) + 8), dict(post_weight=(1 << 20) + 8),
+    dict(gate=(1 << 20) + 8), dict(normed=(1 << 20) + 8)])
+def test_norm_quant_rejects(L, bad):
+    assert L.cider_norm_quant(ctypes.byref(norm_args(**bad)), NULL) == INV
+
+
+def test_norm_quant_empty_and_null(L):
+    assert L.cider_norm_quant(NULL, NULL) == INV
+    assert L.cider_norm_quant(ctypes.byref(cider.NormQuant(M=0, K=64, eps=1e-6, alpha=1.0)), NULL) == 0
+
+
+def test_norm_struct_matches_the_header():
+    import re
+    with open(cider.HEADER_PATH) as f:
+        body = re.search(r"typedef struct \{([^}]*)\} cider_norm_quant_t;", f.read()).group(1)
+    body = re.sub(r"/\*.*?\*/", "", body, flags=re.S)
+    names = [n.strip(" *") for decl in body.split(";") if decl.strip() for n in
+             re.sub(r"^\s*(const )?\w+", "", decl).split(",")]
+    assert names == [f[0] for f in cider.NormQuant._fields_]
+    assert ctypes.sizeof(cider.NormQuant) == 11 * 8 + 4 * 8 + 5 * 4 + 4
+
+
+def test_dequant_rejects(L):
+    d = L.cider_dequant_act
+    assert d(P, P, -1, 64, 0, P, 0, NULL) == INV and d(P, P, 4, 0, 0, P, 0, NULL) == INV
+    assert d(P, P, 4, 100, 64, P, 0, NULL) == INV and d(P, P, 4, 64, 32, P, 0, NULL) == INV
+    assert d(P, P, 4, 64, 0, P, 2, NULL) == INV
+    assert d(NULL, P, 4, 64, 0, P, 0, NULL) == INV and d(P, NULL, 4, 64, 0, P, 0, NULL) == INV
+    assert d(P, P, 4, 64, 0, NULL, 0, NULL) == INV and d(MIS, P, 4, 64, 0, P, 0, NULL) == INV
+    assert d(P, P, 4, 64, 0, MIS, 0, NULL) == INV
+    assert d(NULL, NULL, 0, 64, 0, NULL, 0, NULL) == 0

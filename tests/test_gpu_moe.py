@@ -1,0 +1,381 @@
+"""The routing plan and the products grouped by expert against plain forms in
+64 bits: the plan exactly, the plain products bit for bit (exact integers, two
+fp32 products, one rounding), the gated products within the bound of their
+fp32 steps plus half a step of the output type."""
+import numpy as np
+import pytest
+
+from tests.test_gpu_parity import cider
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+# ---- plan ------------------------------------------------------------------
+
+def plain_plan(ids, E):
+    flat = ids.reshape(-1).astype(np.int64)
+    kept = (flat >= 0) & (flat < E)
+    order = np.argsort(np.where(kept, flat, E), kind="stable")
+    n = int(kept.sum())
+    rows = np.full(flat.size, -1, np.int64)
+    rows[:n] = order[:n]
+    slots = np.full(flat.size, -1, np.int64)
+    slots[order[:n]] = np.arange(n)
+    counts = np.bincount(flat[kept], minlength=E)
+    return np.concatenate([[0], np.cumsum(counts)]), rows, slots.reshape(ids.shape)
+
+
+def check_plan(c, ids, E, **kw):
+    got = c.cider_moe_plan(torch.from_numpy(ids).cuda(), E, **kw)
+    torch.cuda.synchronize()
+    for name, g, o in zip(("offsets", "rows", "slots"), got, plain_plan(ids, E)):
+        assert np.array_equal(g.cpu().numpy(), o), (name, ids.shape, E)
+
+
+@pytest.mark.parametrize("T,k,E", [(0, 2, 5), (1, 1, 1), (1, 8, 64), (3, 3, 7), (63, 1, 2), (65, 2, 512), (129, 8, 128),
+                                   (1024, 8, 64), (1025, 8, 40), (2049, 8, 511), (5000, 3, 96), (40000, 8, 128)])
+def test_plan(T, k, E):
+    c = cider()
+    rng = np.random.default_rng(T * 31 + E)
+    check_plan(c, rng.integers(0, E, (T, k)).astype(np.int32), E)
+    ids = rng.integers(-2, E + 2, (T, k)).astype(np.int32)          # some of no expert
+    ids[rng.random((T, k)) < 0.05] = np.int32(-2 ** 31)
+    ids[rng.random((T, k)) < 0.05] = np.int32(2 ** 31 - 1)
+    check_plan(c, ids, E)
+
+
+@pytest.mark.parametrize("T", [40, 3000])
+def test_plan_one_expert_or_none(T):
+    c = cider()
+    check_plan(c, np.full((T, 4), 6, np.int32), 7)
+    check_plan(c, np.full((T, 4), -1, np.int32), 7)
+    check_plan(c, np.full((T, 4), 7, np.int32), 7)
+
+
+def test_plan_beyond_the_largest_grid_of_chunks():
+    c = cider()
+    rng = np.random.default_rng(3)
+    check_plan(c, rng.integers(-1, 300, (600001, 1)).astype(np.int32), 299)
+
+
+# ---- grouped products ---------------------------------------------------------
+
+DT = {"fp16": torch.float16, "bf16": torch.bfloat16}
+
+
+def unpack(w):
+    return torch.stack(((w & 15).to(torch.int16) - 8, (w >> 4).to(torch.int16) - 8), -1).flatten(-2)
+
+
+def make(counts, N, K, bits, seed, T=None, k=1):
+    """Codes, scales and offsets; with T, a gather index of T rows."""
+    rng = np.random.default_rng(seed)
+    E, P = len(counts), int(sum(counts))
+    xr = P if T is None else T
+    q = lambda *s: torch.from_numpy(np.clip(np.rint(rng.standard_normal(s) * 40), -127, 127).astype(np.int8))  # noqa: E731
+    x = q(xr, K)
+    sx = torch.from_numpy((0.01 + 0.03 * rng.random(xr)).astype(np.float32))
+    if bits == 8:
+        w, s = q(E, N, K), 6e-4
+    else:
+        nib = rng.integers(1, 16, (E, N, K)).astype(np.uint8)       # codes -7 .. 7
+        w, s = torch.from_numpy(nib[..., 0::2] | (nib[..., 1::2] << 4)), 6e-3
+    sw = torch.from_numpy((s * (0.5 + rng.random((E, N)))).astype(np.float32))
+    off = torch.from_numpy(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32))
+    idx = None if T is None else torch.from_numpy(rng.integers(0, T * k, P).astype(np.int32))
+    return x, sx, w, sw, off, idx
+
+
+def plain_values(x, sx, w, sw, off, idx, div, bits):
+    """v [P', N] as the fp32 two-step on exact sums, on the CPU."""
+    codes = w if bits == 8 else unpack(w)
+    out = []
+    for e in range(w.shape[0]):
+        lo, hi = int(off[e]), int(off[e + 1])
+        src = torch.arange(lo, hi) if idx is None else idx[lo:hi].long() // div
+        acc = x[src].double() @ codes[e].double().t()               # exact: |acc| < 2^31
+        out.append((acc.to(torch.float32) * sx[src][:, None]) * sw[e])
+    return torch.cat(out) if out else torch.empty(0, w.shape[1])
+
+
+def call(c, bits, gated, x, sx, w, sw, off, idx, div, **kw):
+    fn = getattr(c, f"cider_w{bits}a8_grouped_{'swiglu' if gated else 'gemm'}")
+    return fn(x.cuda(), sx.cuda(), w.cuda(), sw.cuda(), off.cuda(), row_index=None if idx is None else idx.cuda(),
+              row_div=div, **kw)
+
+
+def assert_gated(y, v, dtype):
+    n = v.shape[1] // 2
+    g, u = v[:, :n].double(), v[:, n:].double()
+    o = g * torch.sigmoid(g) * u
+    # fp32 steps of the activation: (8 + |g|) 2^-23 relative; then half a step
+    # of the output type, or of its smallest number
+    half = torch.finfo(dtype).eps / 2
+    tiny = torch.finfo(dtype).tiny * torch.finfo(dtype).eps / 2
+    bound = o.abs() * (half + (8 + g.abs()) * 2.0 ** -23 * (1 + half)) + tiny + u.abs() * 2.0 ** -118
+    off = (y.double().cpu() - o).abs() - bound
+    assert y.shape == o.shape and bool((off <= 0).all()), float(off.max())
+
+
+COUNTS = {
+    "one": [1], "single rows": [1] * 8, "holes": [0, 5, 0, 0, 17, 1, 0], "edges": [16, 15, 17, 64, 63, 65, 0, 128],
+    "large": [129, 0, 300, 257, 1, 700], "skewed": [0] * 63 + [400] + [1, 2],
+    "many": [(7 * e) % 5 for e in range(500)], "many large": [60 + 9 * (e % 8) for e in range(70)]}
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("name,N,K", [("one", 16, 32), ("one", 1, 160), ("single rows", 200, 1024), ("holes", 136, 96),
+                                      ("holes", 67, 672), ("edges", 264, 416), ("edges", 1003, 128),
+                                      ("large", 520, 288), ("large", 321, 1152), ("skewed", 96, 64), ("many", 40, 64),
+                                      ("many large", 72, 96)])
+def test_grouped_is_the_dense_arithmetic(name, N, K, bits, dtype):
+    c = cider()
+    for T, k in ((None, 1), (37, 3)):
+        a = make(COUNTS[name], N, K, bits, seed=len(name) + N, T=T, k=k)
+        y = call(c, bits, False, *a, k, out_dtype=DT[dtype])
+        o = plain_values(*a, k, bits).to(DT[dtype])
+        assert torch.equal(y.cpu().view(torch.int16), o.view(torch.int16)), (T, k)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("name,N,K", [("one", 2, 32), ("single rows", 416, 1024), ("holes", 130, 672),
+                                      ("edges", 528, 416), ("large", 1040, 288), ("large", 202, 1152),
+                                      ("many", 80, 64), ("many large", 144, 96)])
+def test_swiglu(name, N, K, bits, dtype):
+    c = cider()
+    for T, k in ((None, 1), (37, 3)):
+        a = make(COUNTS[name], N, K, bits, seed=len(name) + N, T=T, k=k)
+        y = call(c, bits, True, *a, k, out_dtype=DT[dtype])
+        assert_gated(y, plain_values(*a, k, bits), DT[dtype])
+
+
+def test_swiglu_of_large_gates():
+    """Gates far in both tails: silu is 0 on the left and the identity on the right."""
+    c = cider()
+    x = torch.full((4, 32), 127, dtype=torch.int8)
+    w = torch.zeros(1, 32, 32, dtype=torch.int8)
+    w[0, :8], w[0, 8:16], w[0, 16:] = 127, -127, 1
+    sx = torch.tensor([1e-4, 1e-3, 1e-2, 1.0])
+    sw = torch.full((1, 32), 1e-3)
+    off = torch.tensor([0, 4], dtype=torch.int32)
+    for t in (torch.float16, torch.bfloat16):
+        y = c.cider_w8a8_grouped_swiglu(x.cuda(), sx.cuda(), w.cuda(), sw.cuda(), off.cuda(), out_dtype=t)
+        v = plain_values(x, sx, w, sw, off, None, 1, 8)
+        assert float(v.abs().max()) > 400.0
+        assert_gated(y, v, t)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("counts", [[3, 0, 9], [40, 70, 0], [200, 0, 310]])
+def test_rows_behind_the_last_group_stay(counts, gated):
+    c = cider()
+    a = make(counts + [7], 64, 96, 8, seed=5)
+    x, sx, w, sw, off, _ = a
+    off = off[:-1].contiguous()                                    # the last 7 rows belong to no expert
+    w, sw = w[:-1].contiguous(), sw[:-1].contiguous()
+    n = 32 if gated else 64
+    y = torch.full((x.shape[0], n), 7.5, dtype=torch.float16, device="cuda")
+    call(c, 8, gated, x, sx, w, sw, off, None, 1, y=y)
+    torch.cuda.synchronize()
+    assert bool((y[int(off[-1]):] == 7.5).all()) and not bool((y[:int(off[-1])] == 7.5).all())
+
+
+def test_no_group_has_rows():
+    c = cider()
+    x, sx, w, sw, _, _ = make([4, 4], 32, 64, 8, seed=6)
+    y = torch.full((8, 32), 7.5, dtype=torch.float16, device="cuda")
+    c.cider_w8a8_grouped_gemm(x.cuda(), sx.cuda(), w.cuda(), sw.cuda(), torch.zeros(3, dtype=torch.int32).cuda(), y=y)
+    torch.cuda.synchronize()
+    assert bool((y == 7.5).all())
+
+
+@pytest.mark.parametrize("counts", [[5, 9], [90, 100], [300, 290]])
+def test_sources_out_of_range_give_zeros(counts):
+    c = cider()
+    x, sx, w, sw, off, idx = make(counts, 48, 128, 8, seed=7, T=20, k=2)
+    idx[::3] = -1
+    idx[1::5] = 40                                                   # // 2 = 20: past the last row
+    idx[2::7] = 2 ** 31 - 1
+    y = call(c, 8, False, x, sx, w, sw, off, idx, 2).cpu()
+    bad = (idx < 0) | (idx >= 40)
+    o = plain_values(x, sx, w, sw, off, torch.where(bad, 0, idx), 2, 8).to(torch.float16)
+    o[bad] = 0.0
+    assert torch.equal(y, o)
+
+
+def test_same_rows_many_times_and_empty_x():
+    c = cider()
+    x, sx, w, sw, off, idx = make([30, 0, 41], 40, 64, 8, seed=8, T=1, k=1)
+    y = call(c, 8, False, x, sx, w, sw, off, idx, 1)
+    assert torch.equal(y.cpu(), plain_values(x, sx, w, sw, off, idx, 1, 8).to(torch.float16))
+    none = torch.empty(0, 64, dtype=torch.int8), torch.empty(0)
+    y = call(c, 8, False, *none, w, sw, off, idx, 1)
+    assert not bool(y.any())
+
+
+def test_offsets_out_of_order_stay_inside_the_buffers():
+    """Clamped, whatever they hold; rows past P are never written."""
+    c = cider()
+    x, sx, w, sw, _, _ = make([64, 64], 64, 64, 8, seed=9)
+    back = torch.full((130, 64), 3.0, dtype=torch.float16, device="cuda")
+    for off in ([0, 500, 128], [-7, 64, 10 ** 9], [2 ** 31 - 1, 0, -2 ** 31], [100, 20, 128]):
+        c.cider_w8a8_grouped_gemm(x.cuda(), sx.cuda(), w.cuda(), sw.cuda(),
+                                  torch.tensor(off, dtype=torch.int64).to(torch.int32).cuda(), y=back[:128])
+        torch.cuda.synchronize()
+        assert bool((back[128:] == 3.0).all())
+
+
+def test_one_expert_is_the_dense_gemm():
+    c = cider()
+    x, sx, w, sw, off, _ = make([333], 640, 512, 8, seed=10)
+    y = call(c, 8, False, x, sx, w, sw, off, None, 1)
+    o = c.cider_w8a8_gemm(x.cuda(), sx.cuda(), w[0].cuda(), sw[0].cuda(), 0)
+    assert torch.equal(y, o)
+
+
+def test_weights_past_4_gib_of_offsets():
+    """Experts behind 2^32 bytes of weights (9 experts of 512 MiB)."""
+    c = cider()
+    E, N, K = 9, 4096, 131072
+    w = torch.zeros(E, N, K, dtype=torch.int8, device="cuda")
+    w[:, :, 0] = torch.arange(1, E + 1, dtype=torch.int8, device="cuda")[:, None]
+    w[:, :, K - 1] = 1
+    x = torch.zeros(E, K, dtype=torch.int8, device="cuda")
+    x[:, 0], x[:, K - 1] = 2, 5
+    one = torch.ones(E, N, device="cuda")
+    y = c.cider_w8a8_grouped_gemm(x, torch.ones(E, device="cuda"), w, one,
+                                  torch.arange(E + 1, dtype=torch.int32, device="cuda"))
+    assert torch.equal(y, (2.0 * torch.arange(1, E + 1, device="cuda") + 5)[:, None].expand(E, N).to(torch.float16))
+
+
+def test_grouped_refuses_other_tensors():
+    c = cider()
+    x, sx, w, sw, off, idx = (t if t is None else t.cuda() for t in make([3, 4], 32, 64, 8, seed=11, T=5))
+    with pytest.raises(ValueError):
+        c.cider_w8a8_grouped_gemm(x, sx, w, sw, off[:-1], row_index=idx)
+    with pytest.raises(TypeError):
+        c.cider_w8a8_grouped_gemm(x, sx, w, sw, off.long(), row_index=idx)
+    with pytest.raises(ValueError):
+        c.cider_w8a8_grouped_gemm(x, sx, w.transpose(1, 2), sw, off, row_index=idx)
+    with pytest.raises(TypeError):
+        c.cider_w8a8_grouped_gemm(x, sx, w, sw, off.cpu(), row_index=idx)
+    with pytest.raises(ValueError):
+        c.cider_w8a8_grouped_swiglu(x, sx, w[:, :31].contiguous(), sw[:, :31].contiguous(), off, row_index=idx)
+    with pytest.raises(c.CiderError):
+        c.cider_w8a8_grouped_gemm(x, sx, w, sw, off, row_index=idx, row_div=0)
+    with pytest.raises(ValueError):
+        c.cider_w8a8_grouped_gemm(x, sx, w, sw, off, row_index=idx, y=torch.empty(8, 32, dtype=torch.float16,
+                                                                                  device="cuda"))
+
+
+# ---- a run of them, as they are used ------------------------------------------
+
+def moe_weights(E, I, H, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    c = cider()
+    gu = (0.02 * torch.randn(E, 2 * I, H, generator=g, device="cuda")).to(torch.bfloat16)
+    dn = (0.02 * torch.randn(E, H, I, generator=g, device="cuda")).to(torch.bfloat16)
+    q = lambda w: tuple(t.view(w.shape[0], w.shape[1], *t.shape[1:]) for t in c.cider_quant_weight(w.flatten(0, 1), 8))  # noqa: E731
+    return q(gu), q(dn)
+
+
+def block(c, x, ids, weights, nw, gu, dn):
+    """norm -> experts -> weighted sum into the residual -> next norm's codes."""
+    _, x_q, x_s = c.cider_norm_quant(x, norm_weight=nw)
+    rows, slots = c.w8a8_moe(x_q, x_s, ids, *gu, *dn, out_dtype=x.dtype)
+    return c.cider_norm_quant(x, rows, nw, slots=slots, weights=weights)
+
+
+def plain_block(x, ids, weights, nw, gu, dn, eps=1e-6):
+    d = lambda q: q[0].double() * q[1].double()[..., None]        # noqa: E731
+    gu, dn, x = d(gu), d(dn), x.double()
+    norm = lambda v: v / torch.sqrt((v * v).mean(1, keepdim=True) + eps) * nw.double()   # noqa: E731
+    quant = lambda v: (lambda s: torch.round(v / s) * s)(v.abs().amax(1, keepdim=True) / 127)   # noqa: E731
+    n = quant(norm(x))
+    out = torch.zeros_like(x)
+    for t in range(x.shape[0]):
+        for j in range(ids.shape[1]):
+            e = int(ids[t, j])
+            if not 0 <= e < gu.shape[0]:
+                continue
+            v = gu[e] @ n[t]
+            g, u = v.chunk(2)
+            a = (g * torch.sigmoid(g) * u).to(torch.bfloat16).double()
+            out[t] += weights[t, j].double() * (dn[e] @ quant(a[None])[0])
+    return x + out
+
+
+@pytest.mark.parametrize("T", [1, 5, 70])
+def test_expert_block(T):
+    c = cider()
+    E, I, H, k = 6, 96, 256, 3
+    g = torch.Generator(device="cuda").manual_seed(T)
+    gu, dn = moe_weights(E, I, H, 20)
+    x = torch.randn(T, H, generator=g, device="cuda").to(torch.bfloat16)
+    ids = torch.rand(T, E, generator=g, device="cuda").topk(k).indices.to(torch.int32)
+    ids[T // 2, 1] = -1
+    w = torch.rand(T, k, generator=g, device="cuda")
+    nw = (1 + 0.1 * torch.randn(H, generator=g, device="cuda")).to(torch.bfloat16)
+    h, x_q, x_s = block(c, x, ids, w, nw, gu, dn)
+    o = plain_block(x, ids, w, nw, gu, dn)
+    # the block's part of h: codes one step off where a value lies on a border
+    # (1/127 of a row's largest value, here at most 3 of them), plus bf16
+    # roundings of a, of the expert rows and of h, each half a step
+    part = (o - x.double()).norm(dim=1)
+    off = (h.double() - o).norm(dim=1)
+    assert bool((off <= 2 ** -8 * o.norm(dim=1) + 0.03 * part).all()), float((off / part).max())
+    assert x_q.shape == (T, H) and x_s.shape == (T,)
+
+
+def test_expert_block_captured_and_replayed():
+    """One capture serves other routings of as many tokens; every replay is the eager result."""
+    c = cider()
+    E, I, H, k, T = 6, 96, 256, 3, 40
+    gu, dn = moe_weights(E, I, H, 21)
+    nw = torch.ones(H, dtype=torch.bfloat16, device="cuda")
+    x = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+    ids = torch.zeros(T, k, dtype=torch.int32, device="cuda")
+    w = torch.zeros(T, k, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        block(c, x, ids, w, nw, gu, dn)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = block(c, x, ids, w, nw, gu, dn)
+    for seed in range(4):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        x.copy_(torch.randn(T, H, generator=g, device="cuda"))
+        ids.copy_(torch.rand(T, E, generator=g, device="cuda").topk(k).indices.to(torch.int32))
+        w.copy_(torch.rand(T, k, generator=g, device="cuda"))
+        if seed == 2:
+            ids[:, 1] = -1
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in out]
+        eager = block(c, x, ids, w, nw, gu, dn)
+        torch.cuda.synchronize()
+        for a, b in zip(got, eager):
+            assert torch.equal(a, b), seed
+
+
+def test_grouped_on_another_stream():
+    c = cider()
+    x, sx, w, sw, off, idx = (t if t is None else t.cuda() for t in make([50, 0, 120], 256, 512, 8, seed=12, T=64, k=2))
+    o = c.cider_w8a8_grouped_gemm(x, sx, w, sw, off, row_index=idx, row_div=2)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    y = c.cider_w8a8_grouped_gemm(x, sx, w, sw, off, row_index=idx, row_div=2, stream=s)
+    ids = torch.randint(0, 5, (3000, 4), dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    plan = c.cider_moe_plan(ids, 5, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(y, o)
+    for a, b in zip(plan, c.cider_moe_plan(ids, 5)):
+        assert torch.equal(a, b)

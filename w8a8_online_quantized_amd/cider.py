@@ -70,6 +70,14 @@ SIGNATURES = {
                                            _c_i64, _c_p, _c_p]),
     "cider_stack_forward_dt": (ctypes.c_int, [_c_p, _c_i32, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_i32, _c_p,
                                               _c_p, _c_i64, _c_p, _c_p]),
+    "cider_moe_plan_workspace_size": (ctypes.c_int64, [_c_i64, _c_i32, _c_i32]),
+    "cider_moe_plan": (ctypes.c_int, [_c_p, _c_i64, _c_i32, _c_i32, _c_p, _c_p, _c_p, _c_p, _c_i64, _c_p]),
+    **{name: (ctypes.c_int, [_c_p, _c_p, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_i32, _c_i64, _c_i64, _c_i64, _c_i32, _c_p,
+                             _c_i32, _c_p])
+       for name in ("cider_w8a8_grouped_gemm", "cider_w4a8_grouped_gemm", "cider_w8a8_grouped_swiglu",
+                    "cider_w4a8_grouped_swiglu")},
+    "cider_norm_quant": (ctypes.c_int, [_c_p, _c_p]),
+    "cider_dequant_act": (ctypes.c_int, [_c_p, _c_p, _c_i64, _c_i64, _c_i32, _c_p, _c_i32, _c_p]),
 }
 
 STACK_PROJECTIONS = ("q", "k", "v", "o", "gate", "up", "down")
@@ -79,6 +87,17 @@ STACK_REGIONS = ("codes", "scales", "q", "k", "v", "o", "gate", "up", "h")
 class StackLayer(ctypes.Structure):
     """cider_stack_layer_t: device pointers of one layer's 7 weight matrices."""
     _fields_ = [("w", ctypes.c_void_p * 7), ("s", ctypes.c_void_p * 7)]
+
+
+
+class NormQuant(ctypes.Structure):
+    """cider_norm_quant_t: device pointers (None leaves a part out) and sizes."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("x", "block", "slots", "weights", "post_weight", "gate", "norm_weight",
+                                               "h", "normed", "x_q", "x_scale")] + \
+               [(n, ctypes.c_int64) for n in ("M", "K", "block_rows", "rows_per_gate")] + \
+               [(n, ctypes.c_int32) for n in ("dtype", "top_k", "group_size")] + \
+               [("alpha", ctypes.c_float), ("eps", ctypes.c_float)]
+
 
 _lib = None
 
@@ -517,6 +536,226 @@ def w4a8_linear(x, w_packed, w_scale, stream=None):
     weights; the output has x's type (fp16 or bf16)."""
     x_q, x_scale = cider_quant_act(x, 0, stream=stream)
     return cider_w4a8_gemm(x_q, x_scale, w_packed, w_scale, stream=stream, out_dtype=x.dtype)
+
+
+# ---- expert blocks ----------------------------------------------------------
+
+def _need_on(dev, t, dtype, shape, name):
+    """_need, and that the tensor lives on the current device `dev`, where the
+    call's kernels run."""
+    _need(t, dtype, shape, name)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the current device {dev}, not {t.get_device()}")
+
+
+def cider_moe_plan_workspace_size(T: int, top_k: int, n_experts: int) -> int:
+    """Workspace bytes cider_moe_plan needs (0: one launch, no workspace)."""
+    n = int(lib().cider_moe_plan_workspace_size(T, top_k, n_experts))
+    if n < 0:
+        raise ValueError("invalid routing sizes")
+    return n
+
+
+@_on_stream
+def cider_moe_plan(expert_ids, n_experts: int, offsets=None, rows=None, slots=None, workspace=None, stream=None):
+    """int32 expert ids [T, top_k] (outside [0, n_experts): no expert) ->
+    (offsets [n_experts + 1], rows [T * top_k], slots [T, top_k]), all int32."""
+    import torch
+    dev = torch.cuda.current_device()
+    T, top_k = expert_ids.shape
+    _need_on(dev, expert_ids, torch.int32, (T, top_k), "expert_ids")
+    need = cider_moe_plan_workspace_size(T, top_k, n_experts)
+    if offsets is None:
+        offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=expert_ids.device)
+    if rows is None:
+        rows = torch.empty(T * top_k, dtype=torch.int32, device=expert_ids.device)
+    if slots is None:
+        slots = torch.empty((T, top_k), dtype=torch.int32, device=expert_ids.device)
+    if need and workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=expert_ids.device)
+    _need_on(dev, offsets, torch.int32, (n_experts + 1,), "offsets")
+    _need_on(dev, rows, torch.int32, (T * top_k,), "rows")
+    _need_on(dev, slots, torch.int32, (T, top_k), "slots")
+    _check("cider_moe_plan", lib().cider_moe_plan(_ptr(expert_ids), T, top_k, n_experts, _ptr(offsets), _ptr(rows),
+                                                  _ptr(slots), *_ws_args(workspace), _stream(stream)))
+    return offsets, rows, slots
+
+
+def _grouped(fn, gated, bits, x_q, x_scale, w, w_scale, offsets, row_index, row_div, y, stream, out_dtype):
+    import torch
+    dev = torch.cuda.current_device()
+    x_rows, K = x_q.shape
+    E, N = w.shape[:2]
+    _need_on(dev, x_q, torch.int8, (x_rows, K), "x_q")
+    _need_on(dev, x_scale, torch.float32, (x_rows,), "x_scale")
+    if bits == 8:
+        _need_on(dev, w, torch.int8, (E, N, K), "w_q")
+    else:
+        _need_on(dev, w, torch.uint8, (E, N, K // 2), "w_packed")
+    _need_on(dev, w_scale, torch.float32, (E, N), "w_scale")
+    _need_on(dev, offsets, torch.int32, (E + 1,), "offsets")
+    P = x_rows
+    if row_index is not None:
+        P = row_index.numel()
+        _need_on(dev, row_index, torch.int32, (P,), "row_index")
+    if gated and N % 2:
+        raise ValueError("the gated product needs as many gate rows as up rows")
+    n_out = N // 2 if gated else N
+    if y is None:
+        y = torch.empty((P, n_out), dtype=out_dtype or torch.float16, device=x_q.device)
+    dt = _fp_code(y, "y")
+    _need_on(dev, y, y.dtype, (P, n_out), "y")
+    _check(fn, getattr(lib(), fn)(_ptr(x_q), _ptr(x_scale), x_rows, _ptr(w), _ptr(w_scale), _ptr(offsets),
+                                  _ptr(row_index), row_div, P, N, K, E, _ptr(y), dt, _stream(stream)))
+    return y
+
+
+@_on_stream
+def cider_w8a8_grouped_gemm(x_q, x_scale, w_q, w_scale, offsets, row_index=None, row_div: int = 1, y=None, stream=None,
+                            out_dtype=None):
+    """Products grouped by expert: rows offsets[e] .. offsets[e+1] - 1 of y
+    [P, N] (fp16, or bf16 when out_dtype or a given y is) are activation rows
+    row_index[p] // row_div (p without an index) times expert e's int8 weights
+    w_q [E, N, K]. offsets int32 [E + 1] on the GPU; rows past its last value
+    are left as they were."""
+    return _grouped("cider_w8a8_grouped_gemm", False, 8, x_q, x_scale, w_q, w_scale, offsets, row_index, row_div, y,
+                    stream, out_dtype)
+
+
+@_on_stream
+def cider_w4a8_grouped_gemm(x_q, x_scale, w_packed, w_scale, offsets, row_index=None, row_div: int = 1, y=None,
+                            stream=None, out_dtype=None):
+    """cider_w8a8_grouped_gemm with packed int4 weights [E, N, K / 2]."""
+    return _grouped("cider_w4a8_grouped_gemm", False, 4, x_q, x_scale, w_packed, w_scale, offsets, row_index, row_div,
+                    y, stream, out_dtype)
+
+
+@_on_stream
+def cider_w8a8_grouped_swiglu(x_q, x_scale, w_q, w_scale, offsets, row_index=None, row_div: int = 1, y=None,
+                              stream=None, out_dtype=None):
+    """The grouped product with the gated activation: weight rows 0 .. N/2 - 1
+    of an expert are gates and the others ups, y [P, N/2] = silu(gate) * up."""
+    return _grouped("cider_w8a8_grouped_swiglu", True, 8, x_q, x_scale, w_q, w_scale, offsets, row_index, row_div, y,
+                    stream, out_dtype)
+
+
+@_on_stream
+def cider_w4a8_grouped_swiglu(x_q, x_scale, w_packed, w_scale, offsets, row_index=None, row_div: int = 1, y=None,
+                              stream=None, out_dtype=None):
+    """cider_w8a8_grouped_swiglu with packed int4 weights [E, N, K / 2]."""
+    return _grouped("cider_w4a8_grouped_swiglu", True, 4, x_q, x_scale, w_packed, w_scale, offsets, row_index, row_div,
+                    y, stream, out_dtype)
+
+
+@_on_stream
+def cider_norm_quant(x=None, block=None, norm_weight=None, slots=None, weights=None, post_weight=None, gate=None,
+                     rows_per_gate: int = 0, alpha: float = 1.0, eps: float = 1e-6, group_size: int = 0, h=None,
+                     normed=None, x_q=None, x_scale=None, stream=None):
+    """The boundary between two blocks -> (h, x_q, x_scale):
+    h = x + alpha * gate * post_norm(block), codes of norm(h). x [M, K] and
+    block [M, K] (or expert rows [R, K] summed by slots and weights [M, top_k])
+    fp16 or bf16; see cider_norm_quant in include/cider.h. Without block, h is
+    x itself; without norm_weight there are no codes (None, None). `normed`, a
+    tensor [M, K], also receives the unquantized norm; h may be x (in place)."""
+    import torch
+    dev = torch.cuda.current_device()
+    lead = x if x is not None else slots if slots is not None else block
+    if lead is None:
+        raise ValueError("x or block must be given")
+    M = lead.shape[0]
+    fp = x if x is not None else block
+    if fp is None:
+        raise ValueError("slots need a block")
+    K, t = fp.shape[1], fp.dtype
+    a = NormQuant(M=M, K=K, dtype=_fp_code(fp, "x"), group_size=group_size, alpha=alpha, eps=eps,
+                  rows_per_gate=rows_per_gate)
+    if group_size and K % group_size:
+        raise ValueError("K must be a multiple of group_size")
+    if x is not None:
+        _need_on(dev, x, t, (M, K), "x")
+        a.x = x.data_ptr()
+    if slots is not None:
+        if block is None:
+            raise ValueError("slots need a block")
+        a.top_k, a.block_rows = slots.shape[1], block.shape[0]
+        _need_on(dev, slots, torch.int32, (M, a.top_k), "slots")
+        _need_on(dev, weights, torch.float32, (M, a.top_k), "weights")
+        a.slots, a.weights = slots.data_ptr(), weights.data_ptr()
+    elif weights is not None:
+        raise ValueError("weights need slots")
+    if block is not None:
+        _need_on(dev, block, t, (a.block_rows if slots is not None else M, K), "block")
+        a.block = block.data_ptr()
+        if h is None:
+            h = torch.empty((M, K), dtype=t, device=fp.device)
+    for name, v in (("post_weight", post_weight), ("norm_weight", norm_weight)):
+        if v is not None:
+            _need_on(dev, v, t, (K,), name)
+            setattr(a, name, v.data_ptr())
+    if gate is not None:
+        if rows_per_gate < 0:
+            raise ValueError("rows_per_gate must not be negative")
+        if rows_per_gate == 0 and gate.dim() == 1:
+            _need_on(dev, gate, t, (K,), "gate")
+        else:
+            _need_on(dev, gate, t, (-(-M // rows_per_gate) if rows_per_gate else 1, K), "gate")
+        a.gate = gate.data_ptr()
+    if h is not None:
+        _need_on(dev, h, t, (M, K), "h")
+        a.h = h.data_ptr()
+    if normed is not None:
+        _need_on(dev, normed, t, (M, K), "normed")
+        a.normed = normed.data_ptr()
+    if norm_weight is not None:
+        if x_q is None:
+            x_q = torch.empty((M, K), dtype=torch.int8, device=fp.device)
+        if x_scale is None:
+            x_scale = torch.empty(_scale_shape(M, K, group_size), dtype=torch.float32, device=fp.device)
+        _need_on(dev, x_q, torch.int8, (M, K), "x_q")
+        _need_on(dev, x_scale, torch.float32, _scale_shape(M, K, group_size), "x_scale")
+        a.x_q, a.x_scale = x_q.data_ptr(), x_scale.data_ptr()
+    elif x_q is not None or x_scale is not None:
+        raise ValueError("codes need a norm_weight")
+    _check("cider_norm_quant", lib().cider_norm_quant(ctypes.byref(a), _stream(stream)))
+    return (h if h is not None else x), x_q, x_scale
+
+
+@_on_stream
+def cider_dequant_act(x_q, x_scale, group_size: int = 0, y=None, stream=None, out_dtype=None):
+    """int8 codes [M, K] and their scales -> rows [M, K], fp16 or (out_dtype or
+    a given y) bf16: what the quantized linears take them to be."""
+    import torch
+    dev = torch.cuda.current_device()
+    M, K = x_q.shape
+    _need_on(dev, x_q, torch.int8, (M, K), "x_q")
+    if group_size and K % group_size:
+        raise ValueError("K must be a multiple of group_size")
+    _need_on(dev, x_scale, torch.float32, _scale_shape(M, K, group_size), "x_scale")
+    if y is None:
+        y = torch.empty((M, K), dtype=out_dtype or torch.float16, device=x_q.device)
+    dt = _fp_code(y, "y")
+    _need_on(dev, y, y.dtype, (M, K), "y")
+    _check("cider_dequant_act", lib().cider_dequant_act(_ptr(x_q), _ptr(x_scale), M, K, group_size, _ptr(y), dt,
+                                                        _stream(stream)))
+    return y
+
+
+@_on_stream
+def w8a8_moe(x_q, x_scale, expert_ids, gate_up, gate_up_scale, down, down_scale, out_dtype=None, stream=None):
+    """The experts of a block on the tokens' codes (from cider_norm_quant or
+    cider_quant_act): gate_up int8 [E, 2I, K] or packed uint8 [E, 2I, K/2],
+    down [E, N, I] likewise. Returns (expert rows [T * top_k, N], slots), which
+    cider_norm_quant sums into the residual."""
+    import torch
+    t = out_dtype or torch.float16
+    top_k, E = expert_ids.shape[1], gate_up.shape[0]
+    offsets, rows, slots = cider_moe_plan(expert_ids, E, stream=stream)
+    up_call = cider_w8a8_grouped_swiglu if gate_up.dtype == torch.int8 else cider_w4a8_grouped_swiglu
+    down_call = cider_w8a8_grouped_gemm if down.dtype == torch.int8 else cider_w4a8_grouped_gemm
+    a = up_call(x_q, x_scale, gate_up, gate_up_scale, offsets, row_index=rows, row_div=top_k, out_dtype=t,
+                stream=stream)
+    a_q, a_scale = cider_quant_act(a, 0, stream=stream)
+    return down_call(a_q, a_scale, down, down_scale, offsets, out_dtype=t, stream=stream), slots
 
 
 def cider_stack_workspace_layout(M: int, hidden: int, q_dim: int, kv_dim: int, mlp_dim: int):

@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 
@@ -577,6 +578,129 @@ cider_status_t cider_stack_forward(const void* x_f16, int64_t M, int64_t hidden,
                                    void* workspace, int64_t workspace_bytes, void* y_f16, void* stream) {
   return cider_stack_forward_dt(x_f16, CIDER_DTYPE_F16, M, hidden, q_dim, kv_dim, mlp_dim, n_layers, layers,
                                 workspace, workspace_bytes, y_f16, stream);
+}
+
+// ---- expert blocks ----------------------------------------------------------
+
+static bool moe_sizes_ok(int64_t T, int32_t top_k, int32_t n_experts) {
+  return T >= 0 && T < (int64_t(1) << 31) && top_k >= 1 && T * top_k < (int64_t(1) << 31) && n_experts >= 1 &&
+         n_experts <= CIDER_MOE_MAX_EXPERTS;
+}
+
+int64_t cider_moe_plan_workspace_size(int64_t T, int32_t top_k, int32_t n_experts) {
+  if (!moe_sizes_ok(T, top_k, n_experts)) return -1;
+  return cider::moe_plan_workspace_bytes(T * top_k, n_experts);
+}
+
+cider_status_t cider_moe_plan(const int32_t* expert_ids, int64_t T, int32_t top_k, int32_t n_experts,
+                              int32_t* offsets, int32_t* rows, int32_t* slots, void* workspace,
+                              int64_t workspace_bytes, void* stream) {
+  if (!moe_sizes_ok(T, top_k, n_experts)) return CIDER_ERROR_INVALID_VALUE;
+  if (!offsets || !aligned16(offsets)) return CIDER_ERROR_INVALID_VALUE;
+  if (T > 0 && (!expert_ids || !rows || !slots)) return CIDER_ERROR_INVALID_VALUE;
+  if (!aligned16(expert_ids) || !aligned16(rows) || !aligned16(slots)) return CIDER_ERROR_INVALID_VALUE;
+  const int64_t need = cider::moe_plan_workspace_bytes(T * top_k, n_experts);
+  if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return CIDER_ERROR_INVALID_VALUE;
+  if (!device_is_gfx950()) return CIDER_ERROR_NOT_SUPPORTED;
+  return from_hip(cider::launch_moe_plan(expert_ids, T * top_k, n_experts, offsets, rows, slots, workspace,
+                                         static_cast<hipStream_t>(stream)));
+}
+
+static cider_status_t grouped_common(const int8_t* x_q, const float* x_scale, int64_t x_rows, const void* w,
+                                     const float* w_scale, const int32_t* offsets, const int32_t* row_index,
+                                     int32_t row_div, int64_t P, int64_t N, int64_t K, int32_t n_experts, void* y,
+                                     int32_t y_dtype, void* stream, cider::WeightKind wk, bool gated) {
+  const bool i4 = wk == cider::kWeightI4;
+  constexpr int64_t kLimit = int64_t(1) << 31;
+  if (!valid_dtype(y_dtype) || !gemm_sizes_ok(P, N) || !valid_k(K, i4 ? 32 : 16, 0)) return CIDER_ERROR_INVALID_VALUE;
+  if (x_rows < 0 || x_rows >= kLimit || row_div < 1 || n_experts < 1 || n_experts > CIDER_MOE_MAX_EXPERTS ||
+      (gated && N % 2 != 0))
+    return CIDER_ERROR_INVALID_VALUE;
+  if (N * (i4 ? K / 2 : K) >= kLimit || (row_index ? x_rows * K >= kLimit : x_rows < P))
+    return CIDER_ERROR_INVALID_VALUE;
+  if (P == 0 || N == 0) return CIDER_SUCCESS;
+  if (!w || !w_scale || !offsets || !y || (x_rows > 0 && (!x_q || !x_scale))) return CIDER_ERROR_INVALID_VALUE;
+  if (!aligned16(x_q) || !aligned16(x_scale) || !aligned16(w) || !aligned16(w_scale) || !aligned16(offsets) ||
+      !aligned16(row_index) || !aligned16(y))
+    return CIDER_ERROR_INVALID_VALUE;
+  const cider::GroupedArgs g{x_q, x_scale, w, w_scale, offsets, row_index, x_rows, P, N, K, row_div, n_experts, y};
+  if (!cider::grouped_launch_fits(g, gated)) return CIDER_ERROR_INVALID_VALUE;
+  if (!device_is_gfx950()) return CIDER_ERROR_NOT_SUPPORTED;
+  return from_hip(cider::launch_grouped(g, wk, y_dtype == CIDER_DTYPE_BF16, gated, static_cast<hipStream_t>(stream)));
+}
+
+cider_status_t cider_w8a8_grouped_gemm(const int8_t* x_q, const float* x_scale, int64_t x_rows, const int8_t* w_q,
+                                       const float* w_scale, const int32_t* offsets, const int32_t* row_index,
+                                       int32_t row_div, int64_t P, int64_t N, int64_t K, int32_t n_experts, void* y,
+                                       int32_t y_dtype, void* stream) {
+  return grouped_common(x_q, x_scale, x_rows, w_q, w_scale, offsets, row_index, row_div, P, N, K, n_experts, y,
+                        y_dtype, stream, cider::kWeightI8, false);
+}
+
+cider_status_t cider_w4a8_grouped_gemm(const int8_t* x_q, const float* x_scale, int64_t x_rows,
+                                       const uint8_t* w_packed, const float* w_scale, const int32_t* offsets,
+                                       const int32_t* row_index, int32_t row_div, int64_t P, int64_t N, int64_t K,
+                                       int32_t n_experts, void* y, int32_t y_dtype, void* stream) {
+  return grouped_common(x_q, x_scale, x_rows, w_packed, w_scale, offsets, row_index, row_div, P, N, K, n_experts, y,
+                        y_dtype, stream, cider::kWeightI4, false);
+}
+
+cider_status_t cider_w8a8_grouped_swiglu(const int8_t* x_q, const float* x_scale, int64_t x_rows, const int8_t* w_q,
+                                         const float* w_scale, const int32_t* offsets, const int32_t* row_index,
+                                         int32_t row_div, int64_t P, int64_t N, int64_t K, int32_t n_experts, void* y,
+                                         int32_t y_dtype, void* stream) {
+  return grouped_common(x_q, x_scale, x_rows, w_q, w_scale, offsets, row_index, row_div, P, N, K, n_experts, y,
+                        y_dtype, stream, cider::kWeightI8, true);
+}
+
+cider_status_t cider_w4a8_grouped_swiglu(const int8_t* x_q, const float* x_scale, int64_t x_rows,
+                                         const uint8_t* w_packed, const float* w_scale, const int32_t* offsets,
+                                         const int32_t* row_index, int32_t row_div, int64_t P, int64_t N, int64_t K,
+                                         int32_t n_experts, void* y, int32_t y_dtype, void* stream) {
+  return grouped_common(x_q, x_scale, x_rows, w_packed, w_scale, offsets, row_index, row_div, P, N, K, n_experts, y,
+                        y_dtype, stream, cider::kWeightI4, true);
+}
+
+cider_status_t cider_norm_quant(const cider_norm_quant_t* args, void* stream) {
+  if (!args) return CIDER_ERROR_INVALID_VALUE;
+  const cider_norm_quant_t& a = *args;
+  // one workgroup of 256 threads per row: the grid stays below 2^31 threads
+  if (!valid_dtype(a.dtype) || a.M < 0 || a.M >= (int64_t(1) << 23) || !valid_gs(a.group_size) ||
+      !valid_k(a.K, 1, a.group_size))
+    return CIDER_ERROR_INVALID_VALUE;
+  if (!std::isfinite(a.alpha) || !std::isfinite(a.eps) || !(a.eps > 0.0f) || a.rows_per_gate < 0)
+    return CIDER_ERROR_INVALID_VALUE;
+  if ((a.slots != nullptr) != (a.weights != nullptr) || (a.x_q != nullptr) != (a.x_scale != nullptr))
+    return CIDER_ERROR_INVALID_VALUE;
+  if (a.slots && (a.top_k < 1 || a.top_k > CIDER_MOE_MAX_TOP_K || a.block_rows < 0 ||
+                  a.block_rows >= (int64_t(1) << 31)))
+    return CIDER_ERROR_INVALID_VALUE;
+  if (a.M == 0) return CIDER_SUCCESS;
+  if (a.block ? !a.h : (!a.x || a.slots || a.post_weight || a.gate)) return CIDER_ERROR_INVALID_VALUE;
+  if ((a.x_q || a.normed) && !a.norm_weight) return CIDER_ERROR_INVALID_VALUE;
+  if (!a.h && !a.x_q && !a.normed) return CIDER_ERROR_INVALID_VALUE;
+  for (const void* p : {a.x, a.block, static_cast<const void*>(a.slots), static_cast<const void*>(a.weights),
+                        a.post_weight, a.gate, a.norm_weight, static_cast<const void*>(a.h),
+                        static_cast<const void*>(a.normed), static_cast<const void*>(a.x_q),
+                        static_cast<const void*>(a.x_scale)})
+    if (!aligned16(p)) return CIDER_ERROR_INVALID_VALUE;
+  if (!device_is_gfx950()) return CIDER_ERROR_NOT_SUPPORTED;
+  const cider::NormArgs n{a.x,      a.block,  a.slots,   a.weights, a.post_weight, a.gate,          a.norm_weight,
+                          a.h,      a.normed, a.x_q,     a.x_scale, a.M,           a.K,             a.block_rows,
+                          a.rows_per_gate,    a.top_k,   a.group_size, a.alpha,    a.eps};
+  return from_hip(cider::launch_norm(n, a.dtype == CIDER_DTYPE_BF16, static_cast<hipStream_t>(stream)));
+}
+
+cider_status_t cider_dequant_act(const int8_t* x_q, const float* x_scale, int64_t M, int64_t K, int32_t group_size,
+                                 void* y, int32_t y_dtype, void* stream) {
+  if (!valid_dtype(y_dtype)) return CIDER_ERROR_INVALID_VALUE;
+  if (M < 0 || !valid_gs(group_size) || !valid_k(K, 1, group_size)) return CIDER_ERROR_INVALID_VALUE;
+  if (M == 0) return CIDER_SUCCESS;
+  if (!x_q || !x_scale || !y || !aligned16(x_q) || !aligned16(x_scale) || !aligned16(y))
+    return CIDER_ERROR_INVALID_VALUE;
+  if (!device_is_gfx950()) return CIDER_ERROR_NOT_SUPPORTED;
+  return from_hip(cider::launch_dequant_rows(x_q, x_scale, M, K, group_size, y, y_dtype == CIDER_DTYPE_BF16,
+                                             static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

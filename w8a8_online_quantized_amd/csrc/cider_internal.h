@@ -90,4 +90,50 @@ hipError_t launch_mv(const MvArgs& args, hipStream_t stream);
 // (written only for an impossible data pattern).
 hipError_t launch_read_probe(const void* buf, int64_t bytes, int32_t* sink, hipStream_t stream);
 
+// Products grouped by expert (int8 or packed int4 weights, per-channel).
+struct GroupedArgs {
+  const int8_t* a;          // activation codes [x_rows, K]
+  const float* sa;          // activation scales [x_rows]
+  const void* w;            // weight codes [E, N, K] int8 or packed [E, N, K/2]
+  const float* sw;          // weight scales [E, N]
+  const int32_t* offsets;   // [E + 1], device
+  const int32_t* row_index; // [P], device, or null: output row p reads activation row row_index[p] / row_div (p)
+  int64_t x_rows, P, N, K;
+  int row_div, E;
+  void* y;                  // [P, N], gated [P, N / 2]
+};
+
+// gated: weight rows 0 .. N/2 - 1 are gates, the others ups. grouped_launch_fits:
+// whether the grid of the output's tiles stays below 2^31 threads.
+bool grouped_launch_fits(const GroupedArgs& args, bool gated);
+hipError_t launch_grouped(const GroupedArgs& args, WeightKind wk, bool bf16, bool gated, hipStream_t stream);
+
+// The routing plan of P = T * top_k expert ids; ws holds moe_plan_workspace_bytes.
+int64_t moe_plan_workspace_bytes(int64_t P, int E);
+hipError_t launch_moe_plan(const int32_t* ids, int64_t P, int E, int32_t* offsets, int32_t* rows, int32_t* slots,
+                           void* ws, hipStream_t stream);
+
+// The boundary between two blocks (null pointers leave a part out).
+struct NormArgs {
+  const void* x;            // residual [M, K]
+  const void* block;        // block output [M, K], or expert rows [block_rows, K] with slots
+  const int32_t* slots;     // [M, top_k]
+  const float* weights;     // [M, top_k]
+  const void* post_weight;  // [K]
+  const void* gate;         // [ceil(M / rows_per_gate), K], [K] with rows_per_gate 0
+  const void* norm_weight;  // [K]
+  void* h;                  // [M, K]
+  void* normed;             // [M, K]
+  int8_t* x_q;              // [M, K]
+  float* x_scale;           // [M] or [M, K / group_size]
+  int64_t M, K, block_rows, rows_per_gate;
+  int top_k, group_size;
+  float alpha, eps;
+};
+hipError_t launch_norm(const NormArgs& args, bool bf16, hipStream_t stream);
+
+// y [M, K] = codes [M, K] times their scales (group_size as for quantizing).
+hipError_t launch_dequant_rows(const int8_t* q, const float* s, int64_t M, int64_t K, int group_size, void* y,
+                               bool bf16, hipStream_t stream);
+
 }  // namespace cider

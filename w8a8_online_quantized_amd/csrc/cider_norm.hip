@@ -1,0 +1,473 @@
+// The boundary between two blocks of a decoder, and the way back from codes:
+//
+//   norm_rows_*      p = post_norm(block), h = x + alpha * gate * p,
+//                    n = norm(h), then the int8 codes of n - one pass over
+//                    the row instead of the five (combine, norm, add, norm,
+//                    quantize) that the parts take
+//   dequant_rows     codes and scales -> fp16 / bf16 rows
+//
+// Mathematics, per row (all in fp32):
+//   p0 = block row, or sum_j weight_j * block[slot_j] (one fma per term, in
+//        j order)
+//   p  = p0 * (1 / sqrt(mean(p0^2) + eps)) * w_post       (with w_post)
+//   h  = round(x + alpha * (gate * p))    to the rows' 16-bit type: the
+//        residual stream is stored in it, and the norm below reads the
+//        stored value, as a program that norms the residual later does
+//   n  = (h * w) * (1 / sqrt(mean(h^2) + eps))
+//   s  = max|n| / 127, codes = clamp(rint(n / s)) by cider_quant_rule.h;
+//        n itself is not rounded to 16 bits before it is quantized.
+// The max over |n| needs no pass of its own: rounding is monotone, so
+// max|fl(t * r)| = fl(max|t| * r) with t = h * w, and max|t| is reduced
+// together with the sum of h^2.
+//
+// HBM-bound: each of x and the block's rows is read once, h and the codes are
+// written once. The row stays in registers from the first load to the codes.
+#include "cider_internal.h"
+#include "cider_quant_rule.h"
+
+namespace cider {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+
+template <bool BF>
+__device__ __forceinline__ uint16_t round16(float v) {
+  if constexpr (BF) return __builtin_bit_cast(uint16_t, (__bf16)v);
+  else return __builtin_bit_cast(uint16_t, (_Float16)v);
+}
+
+template <bool BF>
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = (uint32_t)round16<BF>(v[2 * i]) | ((uint32_t)round16<BF>(v[2 * i + 1]) << 16);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <bool BF>
+__device__ __forceinline__ void unpack8(uint4 q, float (&v)[8]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = elem_to_float<BF>(w[i]);
+    v[2 * i + 1] = elem_to_float<BF>(w[i] >> 16);
+  }
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off);
+  return v;
+}
+
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) v = __builtin_fmaxf(v, __shfl_xor(v, off));
+  return v;
+}
+
+// Sum (and max) over the row's lanes: a wave, or WPR waves through `red`
+// (2 * WPR floats of its own for each call).
+template <int WPR>
+__device__ __forceinline__ void row_reduce(float& sum, float& mx, float* red, int wave, int lane) {
+  sum = wave_sum(sum);
+  mx = wave_max(mx);
+  if constexpr (WPR > 1) {
+    if (lane == 0) {
+      red[wave] = sum;
+      red[WPR + wave] = mx;
+    }
+    __syncthreads();
+    sum = red[0];
+    mx = red[WPR];
+#pragma unroll
+    for (int w = 1; w < WPR; ++w) {
+      sum += red[w];
+      mx = __builtin_fmaxf(mx, red[WPR + w]);
+    }
+  }
+}
+
+__device__ __forceinline__ float inv_rms(float sum, int64_t K, float eps) {
+  return 1.0f / __builtin_sqrtf(sum / (float)K + eps);
+}
+
+// Rows of K % 8 == 0 that fit the registers of a wave (WPR = 1, four rows per
+// workgroup) or of a workgroup of four waves (WPR = 4): CPL 16-byte chunks
+// per lane, chunk L + 64 * WPR * i, so that a wave's loads are contiguous and
+// the 8 or 16 chunks of a scale group are neighbouring lanes.
+template <int CPL, int WPR, bool BF>
+__global__ void __launch_bounds__(kThreads) norm_rows_reg(const NormArgs a) {
+  static_assert(WPR == 1 || WPR == kWaves, "one row per wave or per workgroup");
+  __shared__ float red[2][2 * kWaves];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t row = WPR == 1 ? (int64_t)blockIdx.x * kWaves + wave : (int64_t)blockIdx.x;
+  if (row >= a.M) return;                        // uniform per workgroup when WPR > 1
+  constexpr int kStride = 64 * WPR;
+  const int C = (int)(a.K / 8);
+  const int cl = WPR == 1 ? lane : (int)threadIdx.x;
+
+  // every load that depends on nothing goes out first
+  uint4 xv[CPL], nw[CPL], pw[CPL], gv[CPL];
+  const uint4* xr = static_cast<const uint4*>(a.x) + row * C;
+  const uint4* gr = static_cast<const uint4*>(a.gate) + (a.gate && a.rows_per_gate ? row / a.rows_per_gate * C : 0);
+#pragma unroll
+  for (int i = 0; i < CPL; ++i) {
+    const int c = cl + kStride * i;
+    const uint4 z = make_uint4(0, 0, 0, 0);
+    xv[i] = a.x && c < C ? xr[c] : z;
+    nw[i] = a.norm_weight && c < C ? static_cast<const uint4*>(a.norm_weight)[c] : z;
+    pw[i] = a.post_weight && c < C ? static_cast<const uint4*>(a.post_weight)[c] : z;
+    gv[i] = a.gate && c < C ? gr[c] : z;
+  }
+
+  uint4 hv[CPL];
+  float sum = 0.0f, mx = 0.0f;
+  if (a.block) {
+    float p[CPL][8];
+    if (a.slots) {
+#pragma unroll
+      for (int i = 0; i < CPL; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p[i][e] = 0.0f;
+      constexpr int kAhead = CPL == 1 ? 8 : CPL == 2 ? 4 : 2;   // expert rows in flight
+      for (int j0 = 0; j0 < a.top_k; j0 += kAhead) {
+        uint4 v[kAhead][CPL];
+        float w[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          const bool in = j0 + j < a.top_k;
+          const int64_t at = row * a.top_k + j0 + j;
+          const int slot = in ? a.slots[at] : -1;
+          const bool ok = slot >= 0 && slot < a.block_rows;
+          w[j] = ok ? a.weights[at] : 0.0f;
+          const uint4* br = static_cast<const uint4*>(a.block) + (int64_t)(ok ? slot : 0) * C;
+#pragma unroll
+          for (int i = 0; i < CPL; ++i) {
+            const int c = cl + kStride * i;
+            v[j][i] = ok && c < C ? br[c] : make_uint4(0, 0, 0, 0);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+          for (int i = 0; i < CPL; ++i) {
+            float t[8];
+            unpack8<BF>(v[j][i], t);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[i][e] = __builtin_fmaf(w[j], t[e], p[i][e]);
+          }
+      }
+    } else {
+      const uint4* br = static_cast<const uint4*>(a.block) + row * C;
+#pragma unroll
+      for (int i = 0; i < CPL; ++i) {
+        const int c = cl + kStride * i;
+        unpack8<BF>(c < C ? br[c] : make_uint4(0, 0, 0, 0), p[i]);
+      }
+    }
+    if (a.post_weight) {
+      float s2 = 0.0f, unused = 0.0f;
+#pragma unroll
+      for (int i = 0; i < CPL; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s2 = __builtin_fmaf(p[i][e], p[i][e], s2);
+      row_reduce<WPR>(s2, unused, red[0], wave, lane);
+      const float r = inv_rms(s2, a.K, a.eps);
+#pragma unroll
+      for (int i = 0; i < CPL; ++i) {
+        float w[8];
+        unpack8<BF>(pw[i], w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p[i][e] = p[i][e] * r * w[e];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) {
+      float x[8], g[8], h[8];
+      unpack8<BF>(xv[i], x);
+      unpack8<BF>(gv[i], g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[e] = __builtin_fmaf(a.alpha, a.gate ? g[e] * p[i][e] : p[i][e], x[e]);
+      hv[i] = pack8<BF>(h);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) hv[i] = xv[i];
+  }
+  if (a.h) {
+    uint4* hr = static_cast<uint4*>(a.h) + row * C;
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) {
+      const int c = cl + kStride * i;
+      if (c < C) hr[c] = hv[i];
+    }
+  }
+  if (!a.norm_weight) return;                    // uniform: the residual only
+
+  float t[CPL][8];
+#pragma unroll
+  for (int i = 0; i < CPL; ++i) {
+    float h[8], w[8];
+    unpack8<BF>(hv[i], h);
+    unpack8<BF>(nw[i], w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {                // chunks past the row are zeros
+      sum = __builtin_fmaf(h[e], h[e], sum);
+      t[i][e] = h[e] * w[e];
+      mx = __builtin_fmaxf(mx, __builtin_fabsf(t[i][e]));
+    }
+  }
+  row_reduce<WPR>(sum, mx, red[1], wave, lane);
+  const float r = inv_rms(sum, a.K, a.eps);
+#pragma unroll
+  for (int i = 0; i < CPL; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t[i][e] *= r;
+  if (a.normed) {
+    uint4* nr = static_cast<uint4*>(a.normed) + row * C;
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) {
+      const int c = cl + kStride * i;
+      if (c < C) nr[c] = pack8<BF>(t[i]);
+    }
+  }
+  if (!a.x_q) return;
+  const float row_s = mx * r / 127.0f;
+  const int lpg = a.group_size / 8;              // lanes per scale group, 0: per row
+  if (lpg == 0 && (WPR == 1 ? lane == 0 : threadIdx.x == 0)) a.x_scale[row] = row_s;
+#pragma unroll
+  for (int i = 0; i < CPL; ++i) {
+    const int c = cl + kStride * i;
+    float s = row_s;
+    if (lpg) {
+      float m = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = __builtin_fmaxf(m, __builtin_fabsf(t[i][e]));
+#pragma unroll
+      for (int off = 4; off >= 1; off >>= 1) m = __builtin_fmaxf(m, __shfl_xor(m, off));
+      const float m16 = __builtin_fmaxf(m, __shfl_xor(m, 8));
+      s = (lpg == 16 ? m16 : m) / 127.0f;
+      if ((lane & (lpg - 1)) == 0 && c < C) a.x_scale[row * (C / lpg) + c / lpg] = s;
+    }
+    if (c < C) {
+      const uint2 q = s != 0.0f ? code_bytes_of_values<false>(t[i], s, 1.0f / s, 127.0f) : make_uint2(0, 0);
+      *reinterpret_cast<uint2*>(a.x_q + row * a.K + (int64_t)c * 8) = q;
+    }
+  }
+}
+
+// Rows that fit no register path: K > 8192 (VEC = 8, 16-byte chunks), or K %
+// 8 != 0 (VEC = 1, one element at a time; per-row scale). One workgroup per
+// row, three passes over it: sum of p^2 (with a post-norm), then h, its sum of
+// squares and max|h * w|, then the codes from h read back (each thread reads
+// only what it wrote itself). The block's rows are read twice with a post-norm.
+template <int VEC, bool BF>
+__global__ void __launch_bounds__(kThreads) norm_rows_loop(const NormArgs a) {
+  __shared__ float red[2][2 * kWaves];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t row = blockIdx.x;
+  const int64_t K = a.K;
+  const int64_t gate_at = a.gate && a.rows_per_gate ? row / a.rows_per_gate * K : 0;
+
+  auto load = [&](const void* base, int64_t at, float (&v)[VEC]) {
+    if constexpr (VEC == 8) unpack8<BF>(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at), v);
+    else v[0] = elem_to_float<BF>(static_cast<const uint16_t*>(base)[at]);
+  };
+  auto store = [&](void* base, int64_t at, const float (&v)[VEC]) {
+    if constexpr (VEC == 8) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at) = pack8<BF>(v);
+    else static_cast<uint16_t*>(base)[at] = round16<BF>(v[0]);
+  };
+  auto block_at = [&](int64_t k, float (&p)[VEC]) {
+    if (!a.slots) {
+      load(a.block, row * K + k, p);
+      return;
+    }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) p[e] = 0.0f;
+    for (int j = 0; j < a.top_k; ++j) {
+      const int slot = a.slots[row * a.top_k + j];
+      if (slot < 0 || slot >= a.block_rows) continue;
+      const float w = a.weights[row * a.top_k + j];
+      float v[VEC];
+      load(a.block, (int64_t)slot * K + k, v);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) p[e] = __builtin_fmaf(w, v[e], p[e]);
+    }
+  };
+
+  float r1 = 1.0f;
+  if (a.post_weight) {
+    float s2 = 0.0f, unused = 0.0f;
+    for (int64_t k = (int64_t)threadIdx.x * VEC; k < K; k += kThreads * VEC) {
+      float p[VEC];
+      block_at(k, p);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) s2 = __builtin_fmaf(p[e], p[e], s2);
+    }
+    row_reduce<kWaves>(s2, unused, red[0], wave, lane);
+    r1 = inv_rms(s2, K, a.eps);
+  }
+
+  float sum = 0.0f, mx = 0.0f;
+  for (int64_t k = (int64_t)threadIdx.x * VEC; k < K; k += kThreads * VEC) {
+    float h[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) h[e] = 0.0f;
+    if (a.x) load(a.x, row * K + k, h);
+    if (a.block) {
+      float p[VEC], w[VEC];
+      block_at(k, p);
+      if (a.post_weight) {
+        load(a.post_weight, k, w);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) p[e] = p[e] * r1 * w[e];
+      }
+      if (a.gate) {
+        load(a.gate, gate_at + k, w);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) p[e] *= w[e];
+      }
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) h[e] = elem_to_float<BF>(round16<BF>(__builtin_fmaf(a.alpha, p[e], h[e])));
+    }
+    if (a.h) store(a.h, row * K + k, h);
+    if (a.norm_weight) {
+      float w[VEC];
+      load(a.norm_weight, k, w);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        sum = __builtin_fmaf(h[e], h[e], sum);
+        mx = __builtin_fmaxf(mx, __builtin_fabsf(h[e] * w[e]));
+      }
+    }
+  }
+  if (!a.norm_weight) return;
+  row_reduce<kWaves>(sum, mx, red[1], wave, lane);
+  const float r = inv_rms(sum, K, a.eps);
+  const float row_s = mx * r / 127.0f;
+  const int lpg = a.group_size / 8;
+  if (lpg == 0 && a.x_q && threadIdx.x == 0) a.x_scale[row] = row_s;
+  const void* hsrc = a.h ? a.h : a.x;            // without a block the residual is x itself
+  // every lane of a wave runs the same number of steps: the shuffles below
+  // need all lanes of a group, and groups never straddle the row's end
+  for (int64_t k0 = (int64_t)wave * 64 * VEC; k0 < K; k0 += kThreads * VEC) {
+    const int64_t k = k0 + lane * VEC;
+    const bool in = k < K;
+    float t[VEC], w[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) t[e] = 0.0f;
+    if (in) {
+      load(hsrc, row * K + k, t);
+      load(a.norm_weight, k, w);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) t[e] = t[e] * w[e] * r;
+      if (a.normed) store(a.normed, row * K + k, t);
+    }
+    if (!a.x_q) continue;
+    float s = row_s;
+    if constexpr (VEC == 8) {
+      if (lpg) {
+        float m = 0.0f;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) m = __builtin_fmaxf(m, __builtin_fabsf(t[e]));
+#pragma unroll
+        for (int off = 4; off >= 1; off >>= 1) m = __builtin_fmaxf(m, __shfl_xor(m, off));
+        const float m16 = __builtin_fmaxf(m, __shfl_xor(m, 8));
+        s = (lpg == 16 ? m16 : m) / 127.0f;
+        if (in && (lane & (lpg - 1)) == 0) a.x_scale[row * (K / a.group_size) + k / a.group_size] = s;
+      }
+      if (in)
+        *reinterpret_cast<uint2*>(a.x_q + row * K + k) =
+            s != 0.0f ? code_bytes_of_values<false>(t, s, 1.0f / s, 127.0f) : make_uint2(0, 0);
+    } else {
+      if (in) {
+        float q = s != 0.0f ? __builtin_rintf(t[0] / s) : 0.0f;
+        q = __builtin_fminf(__builtin_fmaxf(q, -127.0f), 127.0f);
+        a.x_q[row * K + k] = (int8_t)q;
+      }
+    }
+  }
+}
+
+template <bool BF>
+hipError_t launch_norm_t(const NormArgs& a, hipStream_t st) {
+  const dim3 block(kThreads);
+  const dim3 rows4((unsigned)((a.M + kWaves - 1) / kWaves)), rows((unsigned)a.M);
+  if (a.K % 8 != 0) norm_rows_loop<1, BF><<<rows, block, 0, st>>>(a);
+  else if (a.K <= 512) norm_rows_reg<1, 1, BF><<<rows4, block, 0, st>>>(a);
+  else if (a.K <= 1024) norm_rows_reg<2, 1, BF><<<rows4, block, 0, st>>>(a);
+  else if (a.K <= 2048) norm_rows_reg<1, kWaves, BF><<<rows, block, 0, st>>>(a);
+  else if (a.K <= 4096) norm_rows_reg<2, kWaves, BF><<<rows, block, 0, st>>>(a);
+  else if (a.K <= 8192) norm_rows_reg<4, kWaves, BF><<<rows, block, 0, st>>>(a);
+  else norm_rows_loop<8, BF><<<rows, block, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+// One code's value as a finished fp32 product (the empty asm keeps the backend
+// from fusing it with the fp16 conversion into one rounding, which bf16 does
+// not have: both types round the same fp32 value).
+__device__ __forceinline__ float code_value(int8_t q, float s) {
+  float v = (float)q * s;
+  asm("" : "+v"(v));
+  return v;
+}
+
+// y = fp(code * scale), 16 codes per thread when rows are whole 16-byte
+// chunks (K % 16 == 0; scale groups are multiples of 16), else one.
+template <int VEC, bool BF>
+__global__ void __launch_bounds__(kThreads) dequant_rows(const int8_t* __restrict__ q, const float* __restrict__ s,
+                                                         int64_t M, int K, int group_size, uint16_t* __restrict__ y) {
+  const int per_row = K / VEC;
+  const int64_t total = M * per_row;
+  const int G = group_size ? K / group_size : 1;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
+    const int64_t row = i / per_row;
+    const int c = (int)(i - row * per_row);
+    const float sc = s[row * G + (group_size ? c * VEC / group_size : 0)];
+    if constexpr (VEC == 16) {
+      const uint4 v = reinterpret_cast<const uint4*>(q)[i];
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      float lo[8], hi[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        lo[e] = code_value((int8_t)(w[e >> 2] >> (8 * (e & 3))), sc);
+        hi[e] = code_value((int8_t)(w[2 + (e >> 2)] >> (8 * (e & 3))), sc);
+      }
+      uint4* dst = reinterpret_cast<uint4*>(y) + 2 * i;
+      dst[0] = pack8<BF>(lo);
+      dst[1] = pack8<BF>(hi);
+    } else {
+      y[i] = round16<BF>(code_value(q[i], sc));
+    }
+  }
+}
+
+template <bool BF>
+hipError_t launch_dequant_t(const int8_t* q, const float* s, int64_t M, int64_t K, int group_size, void* y,
+                            hipStream_t st) {
+  const bool vec = K % 16 == 0;
+  const int64_t items = M * (vec ? K / 16 : K);
+  const unsigned blocks = (unsigned)((items + kThreads - 1) / kThreads < 16384 ? (items + kThreads - 1) / kThreads : 16384);
+  if (vec)
+    dequant_rows<16, BF><<<dim3(blocks), dim3(kThreads), 0, st>>>(q, s, M, (int)K, group_size, static_cast<uint16_t*>(y));
+  else
+    dequant_rows<1, BF><<<dim3(blocks), dim3(kThreads), 0, st>>>(q, s, M, (int)K, group_size, static_cast<uint16_t*>(y));
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_norm(const NormArgs& a, bool bf16, hipStream_t stream) {
+  return bf16 ? launch_norm_t<true>(a, stream) : launch_norm_t<false>(a, stream);
+}
+
+hipError_t launch_dequant_rows(const int8_t* q, const float* s, int64_t M, int64_t K, int group_size, void* y,
+                               bool bf16, hipStream_t stream) {
+  return bf16 ? launch_dequant_t<true>(q, s, M, K, group_size, y, stream)
+              : launch_dequant_t<false>(q, s, M, K, group_size, y, stream);
+}
+
+}  // namespace cider

@@ -45,8 +45,8 @@ __device__ __forceinline__ float elem_to_float(uint32_t bits) {
   else return half_bits_to_float(bits & 0xFFFFu);
 }
 
-// 8 codes of one 16-byte chunk (8 fp16, or bf16 when BF, values) as int8
-// bytes, element j in byte j of the result, by the rule above.
+// 8 codes of 8 values as int8 bytes, element j in byte j of the result, by the
+// rule above.
 // The integer is rounded by adding 1.5 * 2^23: for |r| < 2^22 the sum lands
 // in [2^23, 2^24), where the fp32 spacing is 1, so the round-to-nearest-even
 // addition yields rint(r) (ties to even, as the addend is even) in the low
@@ -60,16 +60,10 @@ __device__ __forceinline__ float elem_to_float(uint32_t bits) {
 // qmax * (1 + 2^-24), so the clamp cannot act and is left out. A scale whose
 // reciprocal is not finite (bf16 groups below ~3.7e-37) sends every element
 // through the division.
-template <bool BF, bool CLAMP>
-__device__ __forceinline__ uint2 code_bytes_of_chunk(uint4 v, float s, float inv, float qmax) {
+template <bool CLAMP>
+__device__ __forceinline__ uint2 code_bytes_of_values(const float (&x)[8], float s, float inv, float qmax) {
   constexpr float kMagic = 12582912.0f;   // 1.5 * 2^23
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  float x[8], r[8], t[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = elem_to_float<BF>(w[i]);
-    x[2 * i + 1] = elem_to_float<BF>(w[i] >> 16);
-  }
+  float r[8], t[8];
   float worst = __builtin_isfinite(inv) ? 0.0f : 1.0f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
@@ -92,6 +86,19 @@ __device__ __forceinline__ uint2 code_bytes_of_chunk(uint4 v, float s, float inv
   o.x = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u) | __builtin_amdgcn_perm(b[3], b[2], 0x04000c0cu);
   o.y = __builtin_amdgcn_perm(b[5], b[4], 0x0c0c0400u) | __builtin_amdgcn_perm(b[7], b[6], 0x04000c0cu);
   return o;
+}
+
+// The same for one 16-byte chunk of fp16 (or bf16 when BF) values.
+template <bool BF, bool CLAMP>
+__device__ __forceinline__ uint2 code_bytes_of_chunk(uint4 v, float s, float inv, float qmax) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = elem_to_float<BF>(w[i]);
+    x[2 * i + 1] = elem_to_float<BF>(w[i] >> 16);
+  }
+  return code_bytes_of_values<CLAMP>(x, s, inv, qmax);
 }
 
 }  // namespace cider
