@@ -153,6 +153,52 @@ def test_swiglu(name, N, K, bits, dtype):
         assert_gated(y, plain_values(*a, k, bits), DT[dtype])
 
 
+# Experts of many rows: several units per block, remainders of every size,
+# tiles cut by N, K that ends inside a stage (the fewest stages among them)
+MANY_ROWS = {
+    "remainders": [255, 257, 512, 0, 17, 1025, 16, 100], "one expert": [1500],
+    "uneven": [0, 0, 3000, 1, 0, 259], "three hundred": [90 + (13 * e) % 60 for e in range(300)],
+    "exact": [256, 512, 256, 768]}
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("name,N,K", [("remainders", 1288, 512), ("remainders", 528, 1120), ("one expert", 2320, 544),
+                                      ("uneven", 272, 704), ("three hundred", 48, 512), ("exact", 1024, 640)])
+def test_experts_of_many_rows(name, N, K, bits, dtype):
+    c = cider()
+    for T, k, gated in ((None, 1, False), (211, 2, True)):
+        a = make(MANY_ROWS[name], N, K, bits, seed=N + K, T=T, k=k)
+        v = plain_values(*a, k, bits)
+        y = call(c, bits, gated, *a, k, out_dtype=DT[dtype])
+        if gated:
+            assert_gated(y, v, DT[dtype])
+        else:
+            assert torch.equal(y.cpu().view(torch.int16), v.to(DT[dtype]).view(torch.int16))
+
+
+# Launches wide enough for the larger tiles (128 x 256, 256 x 192, 256 x 256
+# rows by columns), remainders of several sizes, N that ends inside a tile and
+# off the 16-byte store path, one to four stages of K
+WIDE = [([1399, 0, 1601], 5000, 160), ([1399, 3, 1598], 5003, 400), ([250, 513, 0, 380, 400, 127, 900, 430], 2560, 288),
+        ([2300, 200], 8008, 112), ([3000, 1000], 6000, 240), ([1200], 12301, 400), ([511, 2189, 16], 6160, 512)]
+
+
+@pytest.mark.parametrize("bits,dtype", [(8, "bf16"), (8, "fp16"), (4, "fp16")])
+@pytest.mark.parametrize("counts,N,K", WIDE)
+def test_wide_launches(counts, N, K, bits, dtype):
+    c = cider()
+    K = -(-K // 32) * 32 if bits == 4 else K
+    a = make(counts, N, K, bits, seed=N)
+    y = call(c, bits, False, *a, 1, out_dtype=DT[dtype])
+    v = plain_values(*a, 1, bits)
+    assert torch.equal(y.cpu().view(torch.int16), v.to(DT[dtype]).view(torch.int16))
+    if bits == 8 and dtype == "fp16":
+        return
+    a = make(counts, 2 * N, K, bits, seed=N + 1, T=500, k=2)
+    assert_gated(call(c, bits, True, *a, 2, out_dtype=DT[dtype]), plain_values(*a, 2, bits), DT[dtype])
+
+
 def test_swiglu_of_large_gates():
     """Gates far in both tails: silu is 0 on the left and the identity on the right."""
     c = cider()
@@ -170,10 +216,10 @@ def test_swiglu_of_large_gates():
 
 
 @pytest.mark.parametrize("gated", [False, True])
-@pytest.mark.parametrize("counts", [[3, 0, 9], [40, 70, 0], [200, 0, 310]])
-def test_rows_behind_the_last_group_stay(counts, gated):
+@pytest.mark.parametrize("counts,K", [([3, 0, 9], 96), ([40, 70, 0], 96), ([200, 0, 310], 96), ([200, 0, 310], 640)])
+def test_rows_behind_the_last_group_stay(counts, K, gated):
     c = cider()
-    a = make(counts + [7], 64, 96, 8, seed=5)
+    a = make(counts + [7], 64, K, 8, seed=5)
     x, sx, w, sw, off, _ = a
     off = off[:-1].contiguous()                                    # the last 7 rows belong to no expert
     w, sw = w[:-1].contiguous(), sw[:-1].contiguous()
@@ -193,10 +239,10 @@ def test_no_group_has_rows():
     assert bool((y == 7.5).all())
 
 
-@pytest.mark.parametrize("counts", [[5, 9], [90, 100], [300, 290]])
-def test_sources_out_of_range_give_zeros(counts):
+@pytest.mark.parametrize("counts,K", [([5, 9], 128), ([90, 100], 128), ([300, 290], 128), ([300, 290], 512)])
+def test_sources_out_of_range_give_zeros(counts, K):
     c = cider()
-    x, sx, w, sw, off, idx = make(counts, 48, 128, 8, seed=7, T=20, k=2)
+    x, sx, w, sw, off, idx = make(counts, 48, K, 8, seed=7, T=20, k=2)
     idx[::3] = -1
     idx[1::5] = 40                                                   # // 2 = 20: past the last row
     idx[2::7] = 2 ** 31 - 1
@@ -217,16 +263,17 @@ def test_same_rows_many_times_and_empty_x():
     assert not bool(y.any())
 
 
-def test_offsets_out_of_order_stay_inside_the_buffers():
+@pytest.mark.parametrize("n,K", [(64, 64), (300, 64), (300, 512)])
+def test_offsets_out_of_order_stay_inside_the_buffers(n, K):
     """Clamped, whatever they hold; rows past P are never written."""
     c = cider()
-    x, sx, w, sw, _, _ = make([64, 64], 64, 64, 8, seed=9)
-    back = torch.full((130, 64), 3.0, dtype=torch.float16, device="cuda")
-    for off in ([0, 500, 128], [-7, 64, 10 ** 9], [2 ** 31 - 1, 0, -2 ** 31], [100, 20, 128]):
+    x, sx, w, sw, _, _ = make([n, n], 64, K, 8, seed=9)
+    back = torch.full((2 * n + 2, 64), 3.0, dtype=torch.float16, device="cuda")
+    for off in ([0, 5 * n, 2 * n], [-7, n, 10 ** 9], [2 ** 31 - 1, 0, -2 ** 31], [n + 10, 20, 2 * n]):
         c.cider_w8a8_grouped_gemm(x.cuda(), sx.cuda(), w.cuda(), sw.cuda(),
-                                  torch.tensor(off, dtype=torch.int64).to(torch.int32).cuda(), y=back[:128])
+                                  torch.tensor(off, dtype=torch.int64).to(torch.int32).cuda(), y=back[:2 * n])
         torch.cuda.synchronize()
-        assert bool((back[128:] == 3.0).all())
+        assert bool((back[2 * n:] == 3.0).all())
 
 
 def test_one_expert_is_the_dense_gemm():

@@ -22,7 +22,9 @@
 // resulting list; blocks past its end leave. The grid covers the longest
 // possible list, sum_e ceil(c_e / BM) <= P / BM + min(E, P).
 #include <algorithm>
+#include <type_traits>
 
+#include "../../include/cider.h"
 #include "cider_gemm_common.h"
 #include "cider_internal.h"
 
@@ -51,6 +53,14 @@ __device__ __forceinline__ void group_bounds(const int32_t* __restrict__ offsets
   }
 }
 
+// Activation row of row index i (row_index[p] / row_div), -1 out of range. The
+// division is a multiplication: div_mul = ceil(2^(31 + l) / row_div) with
+// 2^(l - 1) < row_div <= 2^l is exact for every i < 2^31.
+__device__ __forceinline__ int source_of(const GroupedArgs& g, int i) {
+  const int src = g.div_mul ? (int)(__umulhi((uint32_t)i, g.div_mul) >> g.div_shift) : i;
+  return i >= 0 && src < (int)g.x_rows ? src : -1;
+}
+
 struct Unit {
   int e, m0, rows, tn;   // expert, first output row, rows (<= BM), column tile; rows 0: no work
 };
@@ -58,6 +68,7 @@ struct Unit {
 // Work unit of block b: units are (row tile, column tile), column tiles
 // fastest, and each of the 8 XCDs (block b runs on XCD b % 8) takes a
 // contiguous range of them, so that the tiles of one expert share an L2.
+constexpr int kGroupM = 4;
 template <int BM>
 __device__ __forceinline__ Unit find_unit(const int32_t* __restrict__ offsets, int E, int P, int nbn, int b, int lane) {
   Unit u{0, 0, 0, 0};
@@ -76,7 +87,7 @@ __device__ __forceinline__ Unit find_unit(const int32_t* __restrict__ offsets, i
   const int per = units >> 3, rem = units & 7;
   if (idx >= per + (xcd < rem ? 1 : 0)) return u;
   const int unit = xcd < rem ? xcd * (per + 1) + idx : rem * (per + 1) + (xcd - rem) * per + idx;
-  const int mt = unit / nbn;
+  int mt = unit / nbn;
   u.tn = unit - mt * nbn;
   int base = 0, t = t0, incl = incl0;
   for (int g = 0; g < E; g += 64) {
@@ -91,13 +102,37 @@ __device__ __forceinline__ Unit find_unit(const int32_t* __restrict__ offsets, i
       const int l = __builtin_ctzll(hit);
       u.e = g + l;
       const int first = __builtin_amdgcn_readlane(lo, l), last = __builtin_amdgcn_readlane(hi, l);
-      u.m0 = first + (mt - __builtin_amdgcn_readlane(before, l)) * BM;
+      const int start = __builtin_amdgcn_readlane(before, l), n = (last - first + BM - 1) / BM;
+      if (n > kGroupM) {
+        // groups of row tiles, rows fastest within one: the blocks of an XCD
+        // then share both operands' panels
+        const int local = unit - start * nbn, group = local / (kGroupM * nbn), in = local - group * kGroupM * nbn;
+        const int size = min(kGroupM, n - group * kGroupM);
+        u.tn = in / size;
+        mt = start + group * kGroupM + in - u.tn * size;
+      }
+      u.m0 = first + (mt - start) * BM;
       u.rows = min(BM, last - u.m0);
       return u;
     }
     base += __builtin_amdgcn_readlane(incl, 63);
   }
   return u;
+}
+
+// 16 packed int4 codes (8 bytes, nibble = code + 8) as bytes 16 * code, in the
+// order 0,2,4,6 | 1,3,5,7 | 8,10,12,14 | 9,11,13,15: a nibble in a byte's upper
+// half with its top bit flipped is 16 * (nibble - 8) in two's complement, two
+// or three operations for four codes where sign-extending them takes five. The
+// sums stay exact, 16 * 127 * 7 * CIDER_MAX_K < 2^31, and are shifted back once
+// at the end.
+__device__ __forceinline__ v4i unpack16(int lo, int hi) {
+  v4i o;
+  o.x = (int)((((uint32_t)lo << 4) & 0xF0F0F0F0u) ^ 0x80808080u);
+  o.y = (int)(((uint32_t)lo & 0xF0F0F0F0u) ^ 0x80808080u);
+  o.z = (int)((((uint32_t)hi << 4) & 0xF0F0F0F0u) ^ 0x80808080u);
+  o.w = (int)(((uint32_t)hi & 0xF0F0F0F0u) ^ 0x80808080u);
+  return o;
 }
 
 // silu(g) * u of four outputs. exp and the reciprocal are the hardware's
@@ -146,7 +181,9 @@ grouped_kernel(const GroupedArgs g) {
   float* const lsc = reinterpret_cast<float*>(smem + NS * kStageBytes + kPadBytes);
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = (wave % WGM) * WTM, wn = (wave / WGM) * WTN;
+  // waves 0 .. 3 sit on the four SIMDs and share their rows, so a tile with
+  // rows for the first of them only still keeps every SIMD busy
+  const int wm = (wave / WGN) * WTM, wn = (wave % WGN) * WTN;
   const int l16 = lane & 15, l4 = lane >> 4;
   const int N = (int)g.N, K = (int)g.K, NO = GATED ? N / 2 : N;
   const int nbn = (NO + BNO - 1) / BNO;
@@ -162,14 +199,6 @@ grouped_kernel(const GroupedArgs g) {
     const int n = n0 + (r >> 5) * 16 + (r & 15);
     return n < NO ? (r & 16 ? NO + n : n) : -1;
   };
-  // activation row of output row m0 + r, -1 past the group or out of range
-  auto source_row = [&](int r) {
-    if (r >= u.rows) return -1;
-    if (!g.row_index) return u.m0 + r;
-    const int i = g.row_index[u.m0 + r];
-    const int src = i < 0 ? -1 : i / g.row_div;
-    return src < (int)g.x_rows ? src : -1;
-  };
 
   // Descriptors: the expert's whole weight matrix; all activation rows when
   // they are gathered, else the tile's own. A row that does not exist gets an
@@ -182,63 +211,78 @@ grouped_kernel(const GroupedArgs g) {
   const int ca = slot_of<RBA>(wave * (1024 / RBA) + lane / (RBA / 16), lane % (RBA / 16)) * 16;
   const int cw = slot_of<RBW>(wave * (1024 / RBW) + lane / (RBW / 16), lane % (RBW / 16)) * 16;
   uint32_t offa[kIA], offw[kIW];
+  auto issue_a = [&](int kt, int buf) {
+    int8_t* st = smem + buf * kStageBytes;
+    const int kb = kt * BK;
+    const bool none = kb + BK > K && kb + ca >= K;       // chunks past K arrive as zeros
+#pragma unroll
+    for (int i = 0; i < kIA; ++i) {
+      const int j = wave + i * NW;
+      uint32_t off = offa[i] + (uint32_t)kb;             // (an expression in the call leaves the host side without the kernel)
+      if (none) off = kNone;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(kBA % NW != 0 && j >= kBA ? pad : st + j * 1024), 16, off,
+                                               0, 0, 0);
+    }
+  };
+  auto issue_w = [&](int kt, int buf) {
+    int8_t* st = smem + buf * kStageBytes + BM * RBA;
+    const int kb = kt * RBW;
+    const bool none = kb + RBW > (int)ldw && kb + cw >= (int)ldw;
+#pragma unroll
+    for (int i = 0; i < kIW; ++i) {
+      const int j = wave + i * NW;
+      uint32_t off = offw[i] + (uint32_t)kb;
+      if (none) off = kNone;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(kBW % NW != 0 && j >= kBW ? pad : st + j * 1024), 16, off,
+                                               0, 0, 0);
+    }
+  };
+
+  // The row indexes are asked for first and the first weights (which need no
+  // index) go out before they are used: loads complete in order.
+  int ri[kIA];
+#pragma unroll
+  for (int i = 0; i < kIA; ++i) {
+    const int j = wave + i * NW, r = j * (1024 / RBA) + lane / (RBA / 16);
+    ri[i] = j < kBA && r < u.rows ? (g.row_index ? g.row_index[u.m0 + r] : r) : -1;
+  }
+  constexpr int kScalesPerThread = (BM + BN + NW * 64 - 1) / (NW * 64);
+  int rs[kScalesPerThread];                              // scale t of the tile: row t, then column t - BM
+#pragma unroll
+  for (int i = 0; i < kScalesPerThread; ++i) {
+    const int t = threadIdx.x + i * NW * 64;
+    rs[i] = t < BM ? (t < u.rows ? (g.row_index ? g.row_index[u.m0 + t] : u.m0 + t) : -1) : weight_row(t - BM);
+  }
 #pragma unroll
   for (int i = 0; i < kIW; ++i) {
     const int j = wave + i * NW;
     const int r = weight_row(j * (1024 / RBW) + lane / (RBW / 16));
     offw[i] = j < kBW && r >= 0 ? (uint32_t)r * ldw + (uint32_t)cw : kNone;
   }
+  issue_w(0, 0);
+  __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
   for (int i = 0; i < kIA; ++i) {
-    const int j = wave + i * NW;
-    const int r = j * (1024 / RBA) + lane / (RBA / 16);
-    const int src = j < kBA ? source_row(r) : -1;
-    offa[i] = src >= 0 ? (uint32_t)(g.row_index ? src : r) * lda + (uint32_t)ca : kNone;
+    const int src = g.row_index ? source_of(g, ri[i]) : ri[i];
+    offa[i] = src >= 0 ? (uint32_t)src * lda + (uint32_t)ca : kNone;
   }
-
-  auto issue = [&](int kt, int buf) {
-    int8_t* st = smem + buf * kStageBytes;
-    const int kb = kt * BK, kbw = kI4 ? kb / 2 : kb;
-    const bool tail = kb + BK > K;                       // uniform: chunks past K arrive as zeros
-#pragma unroll
-    for (int i = 0; i < kIA; ++i) {
-      const int j = wave + i * NW;
-      uint32_t off = offa[i] + (uint32_t)kb;
-      if (tail && kb + ca >= K) off = kNone;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(kBA % NW != 0 && j >= kBA ? pad : st + j * 1024), 16, off,
-                                               0, 0, 0);
-    }
-#pragma unroll
-    for (int i = 0; i < kIW; ++i) {
-      const int j = wave + i * NW;
-      uint32_t off = offw[i] + (uint32_t)kbw;
-      if (tail && kbw + cw >= (int)ldw) off = kNone;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rw, (lds_void*)(kBW % NW != 0 && j >= kBW ? pad : st + BM * RBA + j * 1024), 16, off, 0, 0, 0);
-    }
-  };
-
   // the tile's scales, zero where there is no row or column: loaded before the
-  // first DMA (loads complete in order), written to LDS behind it
-  constexpr int kScalesPerThread = (BM + BN + NW * 64 - 1) / (NW * 64);
+  // other DMA, written to LDS behind it
   float scl[kScalesPerThread];
 #pragma unroll
   for (int i = 0; i < kScalesPerThread; ++i) {
     const int t = threadIdx.x + i * NW * 64;
-    float v = 0.0f;
-    if (t < BM) {
-      const int src = source_row(t);
-      if (src >= 0) v = g.sa[src];
-    } else if (t < BM + BN) {
-      const int r = weight_row(t - BM);
-      if (r >= 0) v = g.sw[(int64_t)u.e * N + r];
-    }
-    scl[i] = v;
+    const int src = t < BM && g.row_index ? source_of(g, rs[i]) : rs[i];
+    scl[i] = src >= 0 && t < BM + BN ? (t < BM ? g.sa[src] : g.sw[(int64_t)u.e * N + src]) : 0.0f;
   }
+  issue_a(0, 0);
 
   const int KT = (K + BK - 1) / BK;
 #pragma unroll
-  for (int s = 0; s < NS - 1; ++s) issue(s, s);
+  for (int s = 1; s < NS - 1; ++s) {
+    issue_a(s, s);
+    issue_w(s, s);
+  }
 
 #pragma unroll
   for (int i = 0; i < kScalesPerThread; ++i) {
@@ -253,11 +297,111 @@ grouped_kernel(const GroupedArgs g) {
 #pragma unroll
     for (int b = 0; b < TM; ++b) acc[a][b] = zero4();
 
+  // 16-row fragments of this wave that hold rows of the group: the others are
+  // neither read nor multiplied, so a short last tile costs what its rows cost
+  const int nb = min(max((u.rows - wm + 15) >> 4, 0), TM);
+
+  if constexpr (NS == 2) {
+    // Two stages: the next stage's wait, barrier, DMA issue (two stages ahead)
+    // and first fragment reads sit in the middle of the current stage's second
+    // 64-code step, which runs from registers (as in gemm_dma_kernel). Packed
+    // weights are read once per stage, in lane group l4 chunk l4 of their row
+    // (codes 32 l4 .. 32 l4 + 31): step h takes its half h, with activation
+    // chunk 2 l4 + h.
+    auto read_w = [&](const int8_t* st, int ks, int a) {
+      return *reinterpret_cast<const v4i*>(st + BM * RBA + tile_off<RBW>(wn + 16 * a + l16, kI4 ? l4 : 4 * ks + l4));
+    };
+    auto read_a = [&](const int8_t* st, int ks, int b) {
+      return *reinterpret_cast<const v4i*>(st + tile_off<RBA>(wm + 16 * b + l16, kI4 ? 2 * l4 + ks : 4 * ks + l4));
+    };
+    constexpr int kFreeW = TM > TN ? TN : TM - 1;  // the fragment after which all weights have been read
+    wait_vmcnt<0>();
+    stage_barrier();
+    // `full` (every fragment has rows) is a type, so that its loop has no branch
+    // between the reads and MFMAs: at a branch the compiler waits for whatever
+    // either side may have in flight.
+    auto stages = [&](auto full) __attribute__((always_inline)) {
+      v4i wf[TN], af[TM], nwf[TN], naf[TM];
+#pragma unroll
+      for (int a = 0; a < TN; ++a) wf[a] = read_w(smem, 0, a);
+#pragma unroll
+      for (int b = 0; b < 2 && b < TM; ++b) af[b] = read_a(smem, 0, b);
+      __builtin_amdgcn_sched_barrier(0);
+      issue_w(1, 1);
+      issue_a(1, 1);
+      __builtin_amdgcn_sched_barrier(0);
+      for (int kt = 0; kt < KT; ++kt) {
+        const int8_t* st = smem + (kt & 1) * kStageBytes;
+        if constexpr (kI4) {
+#pragma unroll
+          for (int a = 0; a < TN; ++a) {
+            nwf[a] = wf[a];
+            wf[a] = unpack16(nwf[a].x, nwf[a].y);
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < TM; ++b) {
+          if (full.value || b < nb) {
+            const v4i x = kI4 ? even_odd_bytes(af[b]) : af[b];
+#pragma unroll
+            for (int a = 0; a < TN; ++a) acc[a][b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[a], x, acc[a][b], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+            if (b + 2 < TM) af[b + 2] = read_a(st, 0, b + 2);
+            naf[b] = read_a(st, 1, b);
+          }
+          // step 1's weights: one per fragment, the rest with the last one
+#pragma unroll
+          for (int a = b; a < TN && (a == b || b == TM - 1); ++a) {
+            if constexpr (kI4) nwf[a] = unpack16(nwf[a].z, nwf[a].w);
+            else nwf[a] = read_w(st, 1, a);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          if (b == kFreeW) {
+            __builtin_amdgcn_s_waitcnt(0xC07F);
+            stage_barrier();                      // everyone has read stage kt's weights
+            issue_w(kt + 2, kt & 1);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+        constexpr int kHalf = TM / 2;
+#pragma unroll
+        for (int b = 0; b < kHalf; ++b)
+          if (full.value || b < nb) {
+            const v4i x = kI4 ? even_odd_bytes(naf[b]) : naf[b];
+#pragma unroll
+            for (int a = 0; a < TN; ++a) acc[a][b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(nwf[a], x, acc[a][b], 0, 0, 0);
+          }
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(0xC07F);       // own reads of stage kt returned
+        if (kt + 1 < KT) {
+          wait_vmcnt<kIW>();                      // stage kt+1 landed (own DMA)
+          stage_barrier();                        // everyone's: stage kt+1 ready, stage kt free
+          issue_a(kt + 2, kt & 1);                // past the end: zeros that nobody reads
+          const int8_t* sn = smem + ((kt + 1) & 1) * kStageBytes;
+#pragma unroll
+          for (int a = 0; a < TN; ++a) wf[a] = read_w(sn, 0, a);
+#pragma unroll
+          for (int b = 0; b < 2 && b < TM; ++b) af[b] = read_a(sn, 0, b);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int b = kHalf; b < TM; ++b)
+          if (full.value || b < nb) {
+            const v4i x = kI4 ? even_odd_bytes(naf[b]) : naf[b];
+#pragma unroll
+            for (int a = 0; a < TN; ++a) acc[a][b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(nwf[a], x, acc[a][b], 0, 0, 0);
+          }
+      }
+    };
+    if (nb == TM) stages(std::true_type{});
+    else stages(std::false_type{});
+  } else {
   int cur = 0, nxt = NS - 1;                             // buffers of stage kt and of stage kt + NS - 1
   for (int kt = 0; kt < KT; ++kt) {
     wait_vmcnt<(NS - 2) * LPS>();
     stage_barrier();
-    issue(kt + NS - 1, nxt);                             // past the end: zeros that nobody reads
+    issue_a(kt + NS - 1, nxt);                           // past the end: zeros that nobody reads
+    issue_w(kt + NS - 1, nxt);
     const int8_t* sa_ = smem + cur * kStageBytes;
     const int8_t* sw_ = sa_ + BM * RBA;
     nxt = cur;
@@ -273,14 +417,17 @@ grouped_kernel(const GroupedArgs g) {
         for (int b = 0; b < TM; ++b)
           af[b] = *reinterpret_cast<const v4i*>(sa_ + tile_off<RBA>(wm + 16 * b + l16, 4 * ks + l4));
 #pragma unroll
-        for (int a = 0; a < TN; ++a)
+        for (int b = 0; b < TM; ++b)
+          if (TM == 1 || b < nb) {
 #pragma unroll
-          for (int b = 0; b < TM; ++b)
-            acc[a][b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[a], af[b], acc[a][b], 0, 0, 0);
+            for (int a = 0; a < TN; ++a)
+              acc[a][b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[a], af[b], acc[a][b], 0, 0, 0);
+          }
       }
     } else {
       // lane group l4 holds packed chunk l4 of its weight row (codes 32 l4 ..
-      // 32 l4 + 31); half h of it pairs with activation chunk 2 l4 + h
+      // 32 l4 + 31); half h of it pairs with activation chunk 2 l4 + h. The
+      // codes come out times 16 (unpack16).
       v4i wraw[TN];
 #pragma unroll
       for (int a = 0; a < TN; ++a)
@@ -289,19 +436,26 @@ grouped_kernel(const GroupedArgs g) {
       for (int h = 0; h < 2; ++h) {
         v4i wf[TN], af[TM];
 #pragma unroll
-        for (int a = 0; a < TN; ++a)
-          wf[a] = unpack_int4(h ? make_uint2((uint32_t)wraw[a].z, (uint32_t)wraw[a].w)
-                                : make_uint2((uint32_t)wraw[a].x, (uint32_t)wraw[a].y));
+        for (int a = 0; a < TN; ++a) wf[a] = h ? unpack16(wraw[a].z, wraw[a].w) : unpack16(wraw[a].x, wraw[a].y);
 #pragma unroll
         for (int b = 0; b < TM; ++b)
           af[b] = even_odd_bytes(*reinterpret_cast<const v4i*>(sa_ + tile_off<RBA>(wm + 16 * b + l16, 2 * l4 + h)));
 #pragma unroll
-        for (int a = 0; a < TN; ++a)
+        for (int b = 0; b < TM; ++b)
+          if (TM == 1 || b < nb) {
 #pragma unroll
-          for (int b = 0; b < TM; ++b)
-            acc[a][b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[a], af[b], acc[a][b], 0, 0, 0);
+            for (int a = 0; a < TN; ++a)
+              acc[a][b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[a], af[b], acc[a][b], 0, 0, 0);
+          }
       }
     }
+  }
+  }
+  if constexpr (kI4) {
+#pragma unroll
+    for (int a = 0; a < TN; ++a)
+#pragma unroll
+      for (int b = 0; b < TM; ++b) acc[a][b] >>= 4;
   }
   wait_vmcnt<0>();
 
@@ -338,7 +492,7 @@ grouped_kernel(const GroupedArgs g) {
 #pragma unroll
       for (int bl = 0; bl < TM / NP; ++bl) {
         const int b = p * (TM / NP) + bl;
-        const int r0 = (wave % WGM) * RB + 16 * bl;
+        const int r0 = (wave / WGN) * RB + 16 * bl;
         const float sam = lsa[wm + 16 * b + l16];
 #pragma unroll
         for (int a = 0; a < TNO; ++a)
@@ -375,16 +529,41 @@ grouped_kernel(const GroupedArgs g) {
   }
 }
 
-// Tiles by the mean rows of an expert (the group sizes themselves are only
-// known on the device).
+// Tile choice. Only P and the number of experts are known here, not the group
+// sizes: an expert is taken to end in half a tile. Up to 8 rows per expert the
+// weights are read for so few rows that bytes in flight count (three blocks
+// of four stages per CU); above, a launch of T tiles with bpc blocks to a CU runs
+// about ceil(T / (256 bpc)) rounds of bpc * BM * BN * cost, and the cheapest is
+// taken. `cost` (time per tile element and round, relative) was measured on
+// 4096 rows times [12288, 2048] with one expert: 256 x 256 93 us, 256 x 192
+// 101, 128 x 256 117, 64 x 128 154. Measured against forcing each tile: 192
+// rows over 64 experts of 2048 x 2048 43.5 us (32 x 64; 64 x 128 45.2, 16 x 64
+// 47.0, 256 x 256 54), 4096 rows 55.1 (64 x 128; 128 x 256 66, 32 x 64 78,
+// 256 x 256 69), 8192 rows 65.9 (128 x 256; 256 x 192 75, 256 x 256 82), 32768
+// rows 159 (256 x 256; 256 x 192 177, 128 x 256 182), 3000 rows over 8 experts
+// of 2560 x 2560 27.7 (256 x 192; 256 x 256 33, 128 x 256 41).
 struct Tile {
-  int bm, bn, threads;
+  int bm, bn, threads, cost, bpc;
 };
-constexpr Tile kTiles[] = {{16, 64, 128}, {64, 128, 256}, {128, 256, 512}};
+constexpr Tile kTiles[] = {{32, 64, 256, 0, 3}, {64, 128, 512, 100, 3}, {128, 256, 512, 78, 1}, {256, 192, 512, 67, 1},
+                           {256, 256, 512, 62, 1}};
 
-inline int pick_tile(const GroupedArgs& g) {
-  const int64_t mean = g.P / std::min<int64_t>(g.E, g.P);
-  return mean <= 16 ? 0 : mean <= 64 ? 1 : 2;
+inline int pick_tile(const GroupedArgs& g, bool gated) {
+  const int64_t experts = std::min<int64_t>(g.E, g.P);
+  if (g.P <= 8 * experts) return 0;
+  int best = 1;
+  int64_t best_est = 0;
+  for (int i = 1; i < 5; ++i) {
+    const Tile& t = kTiles[i];
+    const int64_t no = gated ? g.N / 2 : g.N, bno = gated ? t.bn / 2 : t.bn;
+    const int64_t tiles = (2 * g.P + experts * t.bm) * ((no + bno - 1) / bno) / (2 * t.bm);
+    const int64_t est = std::max<int64_t>(1, (tiles + 256 * t.bpc - 1) / (256 * t.bpc)) * t.bpc * t.bm * t.bn * t.cost;
+    if (i == 1 || est < best_est) {
+      best = i;
+      best_est = est;
+    }
+  }
+  return best;
 }
 
 // Blocks of the launch: the longest possible list of work units, whole rounds over the XCDs.
@@ -404,10 +583,12 @@ hipError_t launch_tile(const GroupedArgs& g, hipStream_t st) {
 
 template <int WK, bool BF, bool GATED>
 hipError_t launch_t(const GroupedArgs& g, hipStream_t st) {
-  switch (pick_tile(g)) {
-    case 0: return launch_tile<0, 1, 2, 4, WK, BF, GATED>(g, st);
-    case 1: return launch_tile<1, 2, 2, 4, WK, BF, GATED>(g, st);
-    default: return launch_tile<2, 2, 4, 2, WK, BF, GATED>(g, st);
+  switch (pick_tile(g, GATED)) {
+    case 0: return launch_tile<0, 2, 2, 4, WK, BF, GATED>(g, st);
+    case 1: return launch_tile<1, 2, 4, 2, WK, BF, GATED>(g, st);
+    case 2: return launch_tile<2, 2, 4, 2, WK, BF, GATED>(g, st);
+    case 3: return launch_tile<3, 4, 2, 2, WK, BF, GATED>(g, st);
+    default: return launch_tile<4, 2, 4, 2, WK, BF, GATED>(g, st);
   }
 }
 
@@ -420,11 +601,18 @@ hipError_t launch_wk(const GroupedArgs& g, bool bf16, bool gated, hipStream_t st
 }  // namespace
 
 bool grouped_launch_fits(const GroupedArgs& g, bool gated) {
-  const Tile& t = kTiles[pick_tile(g)];
+  const Tile& t = kTiles[pick_tile(g, gated)];
   return grid_blocks(g, t.bm, gated ? t.bn / 2 : t.bn, gated ? g.N / 2 : g.N) < (int64_t(1) << 31) / t.threads;
 }
 
-hipError_t launch_grouped(const GroupedArgs& g, WeightKind wk, bool bf16, bool gated, hipStream_t stream) {
+hipError_t launch_grouped(const GroupedArgs& args, WeightKind wk, bool bf16, bool gated, hipStream_t stream) {
+  GroupedArgs g = args;
+  if (g.row_index && g.row_div > 1) {
+    int l = 1;
+    while ((int64_t(1) << l) < g.row_div) ++l;
+    g.div_mul = (uint32_t)(((uint64_t(1) << (31 + l)) + g.row_div - 1) / g.row_div);
+    g.div_shift = l - 1;
+  }
   return wk == kWeightI4 ? launch_wk<kWeightI4>(g, bf16, gated, stream) : launch_wk<kWeightI8>(g, bf16, gated, stream);
 }
 

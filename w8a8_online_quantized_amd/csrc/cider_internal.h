@@ -101,6 +101,8 @@ struct GroupedArgs {
   int64_t x_rows, P, N, K;
   int row_div, E;
   void* y;                  // [P, N], gated [P, N / 2]
+  uint32_t div_mul = 0;     // row_div as a multiplication (launch_grouped sets it; 0: row_div is 1)
+  int div_shift = 0;
 };
 
 // gated: weight rows 0 .. N/2 - 1 are gates, the others ups. grouped_launch_fits:
