@@ -22,6 +22,11 @@
 //
 // HBM-bound: each of x and the block's rows is read once, h and the codes are
 // written once. The row stays in registers from the first load to the codes.
+// Kernel times (HIP events): 4096 rows of 2560 fp16 with both norms and a gate
+// 17.8 us (73 MB, 4.1 TB/s), 4096 rows of 2048 bf16 each summing 8 expert rows
+// 37.1 us (177 MB, 4.8 TB/s; a plain copy reaches 5.1), one row 4.1 us (an empty
+// launch takes 3.5). Loads as address-space-1 vectors took these from 29.4
+// and 38.9 us: the compiler had made flat one-dword loads of them.
 #include "cider_internal.h"
 #include "cider_quant_rule.h"
 
@@ -37,22 +42,39 @@ __device__ __forceinline__ uint16_t round16(float v) {
   else return __builtin_bit_cast(uint16_t, (_Float16)v);
 }
 
+// 16 bytes at chunk c of a global buffer. (Pointers that arrive in a struct
+// would give flat loads, one dword each where they are conditional.)
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(1))) u4 global_u4;
+
+__device__ __forceinline__ u4 load16(const void* base, int64_t c) { return ((const global_u4*)base)[c]; }
+__device__ __forceinline__ void store16(void* base, int64_t c, u4 v) { ((global_u4*)base)[c] = v; }
+
+// Eight values at once, as vectors: the conversions then come in pairs.
+typedef float f8 __attribute__((ext_vector_type(8)));
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+
 template <bool BF>
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w[i] = (uint32_t)round16<BF>(v[2 * i]) | ((uint32_t)round16<BF>(v[2 * i + 1]) << 16);
-  return make_uint4(w[0], w[1], w[2], w[3]);
+__device__ __forceinline__ u4 pack8(const float (&v)[8]) {
+  const f8 t{v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]};
+  if constexpr (BF) return __builtin_bit_cast(u4, __builtin_convertvector(t, b8));
+  else return __builtin_bit_cast(u4, __builtin_convertvector(t, h8));
 }
 
 template <bool BF>
-__device__ __forceinline__ void unpack8(uint4 q, float (&v)[8]) {
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+__device__ __forceinline__ void unpack8(u4 q, float (&v)[8]) {
+  if constexpr (BF) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = elem_to_float<BF>(w[i]);
-    v[2 * i + 1] = elem_to_float<BF>(w[i] >> 16);
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __builtin_bit_cast(float, w[i] << 16);
+      v[2 * i + 1] = __builtin_bit_cast(float, w[i] & 0xFFFF0000u);
+    }
+  } else {
+    const f8 t = __builtin_convertvector(__builtin_bit_cast(h8, q), f8);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = t[i];
   }
 }
 
@@ -68,8 +90,8 @@ __device__ __forceinline__ float wave_max(float v) {
   return v;
 }
 
-// Sum (and max) over the row's lanes: a wave, or WPR waves through `red`
-// (2 * WPR floats of its own for each call).
+// Sum (and max) over the row's lanes: a wave, or the row's WPR waves through
+// `red` (2 * kWaves floats of its own for each call).
 template <int WPR>
 __device__ __forceinline__ void row_reduce(float& sum, float& mx, float* red, int wave, int lane) {
   sum = wave_sum(sum);
@@ -77,15 +99,16 @@ __device__ __forceinline__ void row_reduce(float& sum, float& mx, float* red, in
   if constexpr (WPR > 1) {
     if (lane == 0) {
       red[wave] = sum;
-      red[WPR + wave] = mx;
+      red[kWaves + wave] = mx;
     }
     __syncthreads();
-    sum = red[0];
-    mx = red[WPR];
+    const int w0 = wave / WPR * WPR;
+    sum = red[w0];
+    mx = red[kWaves + w0];
 #pragma unroll
     for (int w = 1; w < WPR; ++w) {
-      sum += red[w];
-      mx = __builtin_fmaxf(mx, red[WPR + w]);
+      sum += red[w0 + w];
+      mx = __builtin_fmaxf(mx, red[kWaves + w0 + w]);
     }
   }
 }
@@ -94,36 +117,45 @@ __device__ __forceinline__ float inv_rms(float sum, int64_t K, float eps) {
   return 1.0f / __builtin_sqrtf(sum / (float)K + eps);
 }
 
-// Rows of K % 8 == 0 that fit the registers of a wave (WPR = 1, four rows per
-// workgroup) or of a workgroup of four waves (WPR = 4): CPL 16-byte chunks
-// per lane, chunk L + 64 * WPR * i, so that a wave's loads are contiguous and
-// the 8 or 16 chunks of a scale group are neighbouring lanes.
+// Rows of K % 8 == 0 that fit the registers of WPR waves (4 / WPR rows per
+// workgroup): CPL 16-byte chunks per lane, chunk L + 64 * WPR * i, so that a
+// wave's loads are contiguous and the 8 or 16 chunks of a scale group are
+// neighbouring lanes.
 template <int CPL, int WPR, bool BF>
 __global__ void __launch_bounds__(kThreads) norm_rows_reg(const NormArgs a) {
-  static_assert(WPR == 1 || WPR == kWaves, "one row per wave or per workgroup");
+  static_assert(WPR == 1 || WPR == 2 || WPR == kWaves, "rows per workgroup");
   __shared__ float red[2][2 * kWaves];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t row = WPR == 1 ? (int64_t)blockIdx.x * kWaves + wave : (int64_t)blockIdx.x;
-  if (row >= a.M) return;                        // uniform per workgroup when WPR > 1
+  int64_t row = (int64_t)blockIdx.x * (kWaves / WPR) + wave / WPR;
+  if constexpr (WPR == 1) {
+    if (row >= a.M) return;
+  }
+  // a workgroup's second row may not exist: its waves keep the barriers, as a
+  // row of no chunks
+  const int C0 = (int)(a.K / 8), C = row < a.M ? C0 : 0;
+  if (row >= a.M) row = a.M - 1;
   constexpr int kStride = 64 * WPR;
-  const int C = (int)(a.K / 8);
-  const int cl = WPR == 1 ? lane : (int)threadIdx.x;
+  const int cl = (wave % WPR) * 64 + lane;
 
   // every load that depends on nothing goes out first
-  uint4 xv[CPL], nw[CPL], pw[CPL], gv[CPL];
-  const uint4* xr = static_cast<const uint4*>(a.x) + row * C;
-  const uint4* gr = static_cast<const uint4*>(a.gate) + (a.gate && a.rows_per_gate ? row / a.rows_per_gate * C : 0);
+  const u4 z{0, 0, 0, 0};
+  u4 xv[CPL], nw[CPL], pw[CPL], gv[CPL];
+  const int64_t grow = a.gate && a.rows_per_gate ? row / a.rows_per_gate : 0;
 #pragma unroll
-  for (int i = 0; i < CPL; ++i) {
-    const int c = cl + kStride * i;
-    const uint4 z = make_uint4(0, 0, 0, 0);
-    xv[i] = a.x && c < C ? xr[c] : z;
-    nw[i] = a.norm_weight && c < C ? static_cast<const uint4*>(a.norm_weight)[c] : z;
-    pw[i] = a.post_weight && c < C ? static_cast<const uint4*>(a.post_weight)[c] : z;
-    gv[i] = a.gate && c < C ? gr[c] : z;
-  }
+  for (int i = 0; i < CPL; ++i) xv[i] = nw[i] = pw[i] = gv[i] = z;
+  auto load_row = [&](u4 (&v)[CPL], const void* base, int64_t r) {
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) {
+      const int c = cl + kStride * i;
+      if (c < C) v[i] = load16(base, r * C0 + c);
+    }
+  };
+  if (a.x) load_row(xv, a.x, row);
+  if (a.norm_weight) load_row(nw, a.norm_weight, 0);
+  if (a.post_weight) load_row(pw, a.post_weight, 0);
+  if (a.gate) load_row(gv, a.gate, grow);
 
-  uint4 hv[CPL];
+  u4 hv[CPL];
   float sum = 0.0f, mx = 0.0f;
   if (a.block) {
     float p[CPL][8];
@@ -134,7 +166,7 @@ __global__ void __launch_bounds__(kThreads) norm_rows_reg(const NormArgs a) {
         for (int e = 0; e < 8; ++e) p[i][e] = 0.0f;
       constexpr int kAhead = CPL == 1 ? 8 : CPL == 2 ? 4 : 2;   // expert rows in flight
       for (int j0 = 0; j0 < a.top_k; j0 += kAhead) {
-        uint4 v[kAhead][CPL];
+        u4 v[kAhead][CPL];
         float w[kAhead];
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
@@ -143,12 +175,9 @@ __global__ void __launch_bounds__(kThreads) norm_rows_reg(const NormArgs a) {
           const int slot = in ? a.slots[at] : -1;
           const bool ok = slot >= 0 && slot < a.block_rows;
           w[j] = ok ? a.weights[at] : 0.0f;
-          const uint4* br = static_cast<const uint4*>(a.block) + (int64_t)(ok ? slot : 0) * C;
 #pragma unroll
-          for (int i = 0; i < CPL; ++i) {
-            const int c = cl + kStride * i;
-            v[j][i] = ok && c < C ? br[c] : make_uint4(0, 0, 0, 0);
-          }
+          for (int i = 0; i < CPL; ++i) v[j][i] = z;
+          if (ok) load_row(v[j], a.block, slot);
         }
 #pragma unroll
         for (int j = 0; j < kAhead; ++j)
@@ -161,12 +190,12 @@ __global__ void __launch_bounds__(kThreads) norm_rows_reg(const NormArgs a) {
           }
       }
     } else {
-      const uint4* br = static_cast<const uint4*>(a.block) + row * C;
+      u4 v[CPL];
 #pragma unroll
-      for (int i = 0; i < CPL; ++i) {
-        const int c = cl + kStride * i;
-        unpack8<BF>(c < C ? br[c] : make_uint4(0, 0, 0, 0), p[i]);
-      }
+      for (int i = 0; i < CPL; ++i) v[i] = z;
+      load_row(v, a.block, row);
+#pragma unroll
+      for (int i = 0; i < CPL; ++i) unpack8<BF>(v[i], p[i]);
     }
     if (a.post_weight) {
       float s2 = 0.0f, unused = 0.0f;
@@ -184,13 +213,21 @@ __global__ void __launch_bounds__(kThreads) norm_rows_reg(const NormArgs a) {
         for (int e = 0; e < 8; ++e) p[i][e] = p[i][e] * r * w[e];
       }
     }
+    if (a.gate) {
+#pragma unroll
+      for (int i = 0; i < CPL; ++i) {
+        float g[8];
+        unpack8<BF>(gv[i], g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p[i][e] *= g[e];
+      }
+    }
 #pragma unroll
     for (int i = 0; i < CPL; ++i) {
-      float x[8], g[8], h[8];
+      float x[8], h[8];
       unpack8<BF>(xv[i], x);
-      unpack8<BF>(gv[i], g);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[e] = __builtin_fmaf(a.alpha, a.gate ? g[e] * p[i][e] : p[i][e], x[e]);
+      for (int e = 0; e < 8; ++e) h[e] = __builtin_fmaf(a.alpha, p[i][e], x[e]);
       hv[i] = pack8<BF>(h);
     }
   } else {
@@ -198,11 +235,10 @@ __global__ void __launch_bounds__(kThreads) norm_rows_reg(const NormArgs a) {
     for (int i = 0; i < CPL; ++i) hv[i] = xv[i];
   }
   if (a.h) {
-    uint4* hr = static_cast<uint4*>(a.h) + row * C;
 #pragma unroll
     for (int i = 0; i < CPL; ++i) {
       const int c = cl + kStride * i;
-      if (c < C) hr[c] = hv[i];
+      if (c < C) store16(a.h, row * C0 + c, hv[i]);
     }
   }
   if (!a.norm_weight) return;                    // uniform: the residual only
@@ -227,17 +263,16 @@ __global__ void __launch_bounds__(kThreads) norm_rows_reg(const NormArgs a) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) t[i][e] *= r;
   if (a.normed) {
-    uint4* nr = static_cast<uint4*>(a.normed) + row * C;
 #pragma unroll
     for (int i = 0; i < CPL; ++i) {
       const int c = cl + kStride * i;
-      if (c < C) nr[c] = pack8<BF>(t[i]);
+      if (c < C) store16(a.normed, row * C0 + c, pack8<BF>(t[i]));
     }
   }
   if (!a.x_q) return;
   const float row_s = mx * r / 127.0f;
   const int lpg = a.group_size / 8;              // lanes per scale group, 0: per row
-  if (lpg == 0 && (WPR == 1 ? lane == 0 : threadIdx.x == 0)) a.x_scale[row] = row_s;
+  if (lpg == 0 && cl == 0 && C) a.x_scale[row] = row_s;
 #pragma unroll
   for (int i = 0; i < CPL; ++i) {
     const int c = cl + kStride * i;
@@ -250,7 +285,7 @@ __global__ void __launch_bounds__(kThreads) norm_rows_reg(const NormArgs a) {
       for (int off = 4; off >= 1; off >>= 1) m = __builtin_fmaxf(m, __shfl_xor(m, off));
       const float m16 = __builtin_fmaxf(m, __shfl_xor(m, 8));
       s = (lpg == 16 ? m16 : m) / 127.0f;
-      if ((lane & (lpg - 1)) == 0 && c < C) a.x_scale[row * (C / lpg) + c / lpg] = s;
+      if ((lane & (lpg - 1)) == 0 && c < C) a.x_scale[row * (C0 / lpg) + c / lpg] = s;
     }
     if (c < C) {
       const uint2 q = s != 0.0f ? code_bytes_of_values<false>(t[i], s, 1.0f / s, 127.0f) : make_uint2(0, 0);
@@ -273,11 +308,11 @@ __global__ void __launch_bounds__(kThreads) norm_rows_loop(const NormArgs a) {
   const int64_t gate_at = a.gate && a.rows_per_gate ? row / a.rows_per_gate * K : 0;
 
   auto load = [&](const void* base, int64_t at, float (&v)[VEC]) {
-    if constexpr (VEC == 8) unpack8<BF>(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at), v);
+    if constexpr (VEC == 8) unpack8<BF>(load16(base, at / 8), v);
     else v[0] = elem_to_float<BF>(static_cast<const uint16_t*>(base)[at]);
   };
   auto store = [&](void* base, int64_t at, const float (&v)[VEC]) {
-    if constexpr (VEC == 8) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at) = pack8<BF>(v);
+    if constexpr (VEC == 8) store16(base, at / 8, pack8<BF>(v));
     else static_cast<uint16_t*>(base)[at] = round16<BF>(v[0]);
   };
   auto block_at = [&](int64_t k, float (&p)[VEC]) {
@@ -394,15 +429,23 @@ __global__ void __launch_bounds__(kThreads) norm_rows_loop(const NormArgs a) {
 
 template <bool BF>
 hipError_t launch_norm_t(const NormArgs& a, hipStream_t st) {
+  // Waves and chunks per row: as few as hold the row up to K = 1024, then four
+  // waves (4096 rows of K = 2048, one wave of 4 chunks per lane 19.5 us, two
+  // waves 13.3, four 13.0; one row 7.5 / 5.2 / 4.1), but two where four would
+  // leave most of their second chunks idle (K = 2560: four waves of 2 chunks
+  // 17.1 us, two of 3 16.5, one of 5 18.0).
   const dim3 block(kThreads);
-  const dim3 rows4((unsigned)((a.M + kWaves - 1) / kWaves)), rows((unsigned)a.M);
-  if (a.K % 8 != 0) norm_rows_loop<1, BF><<<rows, block, 0, st>>>(a);
-  else if (a.K <= 512) norm_rows_reg<1, 1, BF><<<rows4, block, 0, st>>>(a);
-  else if (a.K <= 1024) norm_rows_reg<2, 1, BF><<<rows4, block, 0, st>>>(a);
-  else if (a.K <= 2048) norm_rows_reg<1, kWaves, BF><<<rows, block, 0, st>>>(a);
-  else if (a.K <= 4096) norm_rows_reg<2, kWaves, BF><<<rows, block, 0, st>>>(a);
-  else if (a.K <= 8192) norm_rows_reg<4, kWaves, BF><<<rows, block, 0, st>>>(a);
-  else norm_rows_loop<8, BF><<<rows, block, 0, st>>>(a);
+  const unsigned rows1 = (unsigned)a.M, rows2 = (rows1 + 1) / 2, rows4 = (rows1 + 3) / 4;
+  const int64_t C = a.K / 8;                     // 16-byte chunks per row
+  if (a.K % 8 != 0) norm_rows_loop<1, BF><<<dim3(rows1), block, 0, st>>>(a);
+  else if (C <= 64) norm_rows_reg<1, 1, BF><<<dim3(rows4), block, 0, st>>>(a);
+  else if (C <= 128) norm_rows_reg<2, 1, BF><<<dim3(rows4), block, 0, st>>>(a);
+  else if (C <= 256) norm_rows_reg<1, kWaves, BF><<<dim3(rows1), block, 0, st>>>(a);
+  else if (C <= 384) norm_rows_reg<3, 2, BF><<<dim3(rows2), block, 0, st>>>(a);
+  else if (C <= 512) norm_rows_reg<2, kWaves, BF><<<dim3(rows1), block, 0, st>>>(a);
+  else if (C <= 768) norm_rows_reg<3, kWaves, BF><<<dim3(rows1), block, 0, st>>>(a);
+  else if (C <= 1024) norm_rows_reg<4, kWaves, BF><<<dim3(rows1), block, 0, st>>>(a);
+  else norm_rows_loop<8, BF><<<dim3(rows1), block, 0, st>>>(a);
   return hipGetLastError();
 }
 
@@ -436,9 +479,8 @@ __global__ void __launch_bounds__(kThreads) dequant_rows(const int8_t* __restric
         lo[e] = code_value((int8_t)(w[e >> 2] >> (8 * (e & 3))), sc);
         hi[e] = code_value((int8_t)(w[2 + (e >> 2)] >> (8 * (e & 3))), sc);
       }
-      uint4* dst = reinterpret_cast<uint4*>(y) + 2 * i;
-      dst[0] = pack8<BF>(lo);
-      dst[1] = pack8<BF>(hi);
+      store16(y, 2 * i, pack8<BF>(lo));
+      store16(y, 2 * i + 1, pack8<BF>(hi));
     } else {
       y[i] = round16<BF>(code_value(q[i], sc));
     }
