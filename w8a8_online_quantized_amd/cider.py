@@ -539,18 +539,30 @@ def w4a8_linear(x, w_packed, w_scale, stream=None):
 
 
 # ---- expert blocks ----------------------------------------------------------
+# A decode step runs these on a few rows, where the call costs more than its
+# kernel: tensors that fit are passed with one test each, and pointers go to
+# ctypes as plain integers.
 
 def _need_on(dev, t, dtype, shape, name):
     """_need, and that the tensor lives on the current device `dev`, where the
     call's kernels run."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return
+    except AttributeError:
+        pass                                        # not a tensor: _need says so
     _need(t, dtype, shape, name)
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on the current device {dev}, not {t.get_device()}")
+    raise ValueError(f"{name} must be on the current device {dev}, not {t.get_device()}")
+
+
+def _raw_stream(stream, dev):
+    import torch
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def cider_moe_plan_workspace_size(T: int, top_k: int, n_experts: int) -> int:
     """Workspace bytes cider_moe_plan needs (0: one launch, no workspace)."""
-    n = int(lib().cider_moe_plan_workspace_size(T, top_k, n_experts))
+    n = lib().cider_moe_plan_workspace_size(T, top_k, n_experts)
     if n < 0:
         raise ValueError("invalid routing sizes")
     return n
@@ -562,22 +574,27 @@ def cider_moe_plan(expert_ids, n_experts: int, offsets=None, rows=None, slots=No
     (offsets [n_experts + 1], rows [T * top_k], slots [T, top_k]), all int32."""
     import torch
     dev = torch.cuda.current_device()
-    T, top_k = expert_ids.shape
-    _need_on(dev, expert_ids, torch.int32, (T, top_k), "expert_ids")
+    T, top_k = shape = expert_ids.shape
+    _need_on(dev, expert_ids, torch.int32, shape, "expert_ids")
     need = cider_moe_plan_workspace_size(T, top_k, n_experts)
     if offsets is None:
         offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=expert_ids.device)
+    else:
+        _need_on(dev, offsets, torch.int32, (n_experts + 1,), "offsets")
     if rows is None:
         rows = torch.empty(T * top_k, dtype=torch.int32, device=expert_ids.device)
+    else:
+        _need_on(dev, rows, torch.int32, (T * top_k,), "rows")
     if slots is None:
-        slots = torch.empty((T, top_k), dtype=torch.int32, device=expert_ids.device)
+        slots = torch.empty(shape, dtype=torch.int32, device=expert_ids.device)
+    else:
+        _need_on(dev, slots, torch.int32, shape, "slots")
     if need and workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=expert_ids.device)
-    _need_on(dev, offsets, torch.int32, (n_experts + 1,), "offsets")
-    _need_on(dev, rows, torch.int32, (T * top_k,), "rows")
-    _need_on(dev, slots, torch.int32, (T, top_k), "slots")
-    _check("cider_moe_plan", lib().cider_moe_plan(_ptr(expert_ids), T, top_k, n_experts, _ptr(offsets), _ptr(rows),
-                                                  _ptr(slots), *_ws_args(workspace), _stream(stream)))
+    st = lib().cider_moe_plan(expert_ids.data_ptr(), T, top_k, n_experts, offsets.data_ptr(), rows.data_ptr(),
+                              slots.data_ptr(), *_ws_args(workspace), _raw_stream(stream, dev))
+    if st:
+        _check("cider_moe_plan", st)
     return offsets, rows, slots
 
 
@@ -585,7 +602,7 @@ def _grouped(fn, gated, bits, x_q, x_scale, w, w_scale, offsets, row_index, row_
     import torch
     dev = torch.cuda.current_device()
     x_rows, K = x_q.shape
-    E, N = w.shape[:2]
+    E, N = w_scale.shape
     _need_on(dev, x_q, torch.int8, (x_rows, K), "x_q")
     _need_on(dev, x_scale, torch.float32, (x_rows,), "x_scale")
     if bits == 8:
@@ -594,19 +611,22 @@ def _grouped(fn, gated, bits, x_q, x_scale, w, w_scale, offsets, row_index, row_
         _need_on(dev, w, torch.uint8, (E, N, K // 2), "w_packed")
     _need_on(dev, w_scale, torch.float32, (E, N), "w_scale")
     _need_on(dev, offsets, torch.int32, (E + 1,), "offsets")
-    P = x_rows
+    P, index = x_rows, None
     if row_index is not None:
-        P = row_index.numel()
+        P, index = row_index.numel(), row_index.data_ptr()
         _need_on(dev, row_index, torch.int32, (P,), "row_index")
     if gated and N % 2:
         raise ValueError("the gated product needs as many gate rows as up rows")
     n_out = N // 2 if gated else N
     if y is None:
         y = torch.empty((P, n_out), dtype=out_dtype or torch.float16, device=x_q.device)
-    dt = _fp_code(y, "y")
-    _need_on(dev, y, y.dtype, (P, n_out), "y")
-    _check(fn, getattr(lib(), fn)(_ptr(x_q), _ptr(x_scale), x_rows, _ptr(w), _ptr(w_scale), _ptr(offsets),
-                                  _ptr(row_index), row_div, P, N, K, E, _ptr(y), dt, _stream(stream)))
+    else:
+        _need_on(dev, y, y.dtype, (P, n_out), "y")
+    st = getattr(lib(), fn)(x_q.data_ptr(), x_scale.data_ptr(), x_rows, w.data_ptr(), w_scale.data_ptr(),
+                            offsets.data_ptr(), index, row_div, P, N, K, E, y.data_ptr(), _fp_code(y, "y"),
+                            _raw_stream(stream, dev))
+    if st:
+        _check(fn, st)
     return y
 
 
@@ -659,64 +679,68 @@ def cider_norm_quant(x=None, block=None, norm_weight=None, slots=None, weights=N
     tensor [M, K], also receives the unquantized norm; h may be x (in place)."""
     import torch
     dev = torch.cuda.current_device()
-    lead = x if x is not None else slots if slots is not None else block
-    if lead is None:
-        raise ValueError("x or block must be given")
-    M = lead.shape[0]
     fp = x if x is not None else block
     if fp is None:
-        raise ValueError("slots need a block")
+        raise ValueError("x or block must be given")
     K, t = fp.shape[1], fp.dtype
-    a = NormQuant(M=M, K=K, dtype=_fp_code(fp, "x"), group_size=group_size, alpha=alpha, eps=eps,
-                  rows_per_gate=rows_per_gate)
+    M = fp.shape[0] if x is not None or slots is None else slots.shape[0]
     if group_size and K % group_size:
         raise ValueError("K must be a multiple of group_size")
+    row, vec = (M, K), (K,)
+    top_k = block_rows = 0
+    px = pb = ps = pw = pp = pg = pn = ph = pd = pq = pc = None
     if x is not None:
-        _need_on(dev, x, t, (M, K), "x")
-        a.x = x.data_ptr()
+        _need_on(dev, x, t, row, "x")
+        px = x.data_ptr()
     if slots is not None:
         if block is None:
             raise ValueError("slots need a block")
-        a.top_k, a.block_rows = slots.shape[1], block.shape[0]
-        _need_on(dev, slots, torch.int32, (M, a.top_k), "slots")
-        _need_on(dev, weights, torch.float32, (M, a.top_k), "weights")
-        a.slots, a.weights = slots.data_ptr(), weights.data_ptr()
+        top_k, block_rows = slots.shape[1], block.shape[0]
+        _need_on(dev, slots, torch.int32, (M, top_k), "slots")
+        _need_on(dev, weights, torch.float32, (M, top_k), "weights")
+        ps, pw = slots.data_ptr(), weights.data_ptr()
     elif weights is not None:
         raise ValueError("weights need slots")
     if block is not None:
-        _need_on(dev, block, t, (a.block_rows if slots is not None else M, K), "block")
-        a.block = block.data_ptr()
+        _need_on(dev, block, t, (block_rows, K) if slots is not None else row, "block")
+        pb = block.data_ptr()
         if h is None:
-            h = torch.empty((M, K), dtype=t, device=fp.device)
-    for name, v in (("post_weight", post_weight), ("norm_weight", norm_weight)):
-        if v is not None:
-            _need_on(dev, v, t, (K,), name)
-            setattr(a, name, v.data_ptr())
+            h = torch.empty(row, dtype=t, device=fp.device)
+    if post_weight is not None:
+        _need_on(dev, post_weight, t, vec, "post_weight")
+        pp = post_weight.data_ptr()
     if gate is not None:
         if rows_per_gate < 0:
             raise ValueError("rows_per_gate must not be negative")
-        if rows_per_gate == 0 and gate.dim() == 1:
-            _need_on(dev, gate, t, (K,), "gate")
-        else:
-            _need_on(dev, gate, t, (-(-M // rows_per_gate) if rows_per_gate else 1, K), "gate")
-        a.gate = gate.data_ptr()
+        one = rows_per_gate == 0 and gate.dim() == 1
+        _need_on(dev, gate, t, vec if one else (-(-M // rows_per_gate) if rows_per_gate else 1, K), "gate")
+        pg = gate.data_ptr()
     if h is not None:
-        _need_on(dev, h, t, (M, K), "h")
-        a.h = h.data_ptr()
+        _need_on(dev, h, t, row, "h")
+        ph = h.data_ptr()
     if normed is not None:
-        _need_on(dev, normed, t, (M, K), "normed")
-        a.normed = normed.data_ptr()
+        _need_on(dev, normed, t, row, "normed")
+        pd = normed.data_ptr()
     if norm_weight is not None:
+        _need_on(dev, norm_weight, t, vec, "norm_weight")
+        pn = norm_weight.data_ptr()
+        scales = _scale_shape(M, K, group_size)
         if x_q is None:
-            x_q = torch.empty((M, K), dtype=torch.int8, device=fp.device)
+            x_q = torch.empty(row, dtype=torch.int8, device=fp.device)
+        else:
+            _need_on(dev, x_q, torch.int8, row, "x_q")
         if x_scale is None:
-            x_scale = torch.empty(_scale_shape(M, K, group_size), dtype=torch.float32, device=fp.device)
-        _need_on(dev, x_q, torch.int8, (M, K), "x_q")
-        _need_on(dev, x_scale, torch.float32, _scale_shape(M, K, group_size), "x_scale")
-        a.x_q, a.x_scale = x_q.data_ptr(), x_scale.data_ptr()
+            x_scale = torch.empty(scales, dtype=torch.float32, device=fp.device)
+        else:
+            _need_on(dev, x_scale, torch.float32, scales, "x_scale")
+        pq, pc = x_q.data_ptr(), x_scale.data_ptr()
     elif x_q is not None or x_scale is not None:
         raise ValueError("codes need a norm_weight")
-    _check("cider_norm_quant", lib().cider_norm_quant(ctypes.byref(a), _stream(stream)))
+    args = NormQuant(px, pb, ps, pw, pp, pg, pn, ph, pd, pq, pc, M, K, block_rows, rows_per_gate, _fp_code(fp, "x"),
+                     top_k, group_size, alpha, eps)
+    st = lib().cider_norm_quant(ctypes.byref(args), _raw_stream(stream, dev))
+    if st:
+        _check("cider_norm_quant", st)
     return (h if h is not None else x), x_q, x_scale
 
 
@@ -726,17 +750,19 @@ def cider_dequant_act(x_q, x_scale, group_size: int = 0, y=None, stream=None, ou
     a given y) bf16: what the quantized linears take them to be."""
     import torch
     dev = torch.cuda.current_device()
-    M, K = x_q.shape
-    _need_on(dev, x_q, torch.int8, (M, K), "x_q")
+    M, K = row = x_q.shape
+    _need_on(dev, x_q, torch.int8, row, "x_q")
     if group_size and K % group_size:
         raise ValueError("K must be a multiple of group_size")
     _need_on(dev, x_scale, torch.float32, _scale_shape(M, K, group_size), "x_scale")
     if y is None:
-        y = torch.empty((M, K), dtype=out_dtype or torch.float16, device=x_q.device)
-    dt = _fp_code(y, "y")
-    _need_on(dev, y, y.dtype, (M, K), "y")
-    _check("cider_dequant_act", lib().cider_dequant_act(_ptr(x_q), _ptr(x_scale), M, K, group_size, _ptr(y), dt,
-                                                        _stream(stream)))
+        y = torch.empty(row, dtype=out_dtype or torch.float16, device=x_q.device)
+    else:
+        _need_on(dev, y, y.dtype, row, "y")
+    st = lib().cider_dequant_act(x_q.data_ptr(), x_scale.data_ptr(), M, K, group_size, y.data_ptr(), _fp_code(y, "y"),
+                                 _raw_stream(stream, dev))
+    if st:
+        _check("cider_dequant_act", st)
     return y
 
 
