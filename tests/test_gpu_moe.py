@@ -426,3 +426,107 @@ def test_grouped_on_another_stream():
     assert torch.equal(y, o)
     for a, b in zip(plan, c.cider_moe_plan(ids, 5)):
         assert torch.equal(a, b)
+
+
+def test_expert_block_of_no_tokens():
+    c = cider()
+    gu, dn = moe_weights(4, 32, 64, 22)
+    x = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
+    ids = torch.empty(0, 2, dtype=torch.int32, device="cuda")
+    h, x_q, x_s = block(c, x, ids, torch.empty(0, 2, device="cuda"), torch.ones(64, dtype=torch.bfloat16, device="cuda"),
+                        gu, dn)
+    torch.cuda.synchronize()
+    assert h.shape == x_q.shape == (0, 64) and x_s.shape == (0,)
+
+
+@pytest.mark.parametrize("T", [1, 33])
+def test_expert_rows_of_packed_weights(T):
+    """w8a8_moe on packed int4 experts is its parts, one expert's rows after another on the dense entries."""
+    c = cider()
+    E, I, H, k = 5, 160, 224, 2
+    rng = np.random.default_rng(T)
+    x, sx, gu, sgu, _, _ = (t if t is None else t.cuda() for t in make([T] + [0] * (E - 1), 2 * I, H, 4, seed=30))
+    _, _, dn, sdn, _, _ = (t if t is None else t.cuda() for t in make([1] + [0] * (E - 1), H, I, 4, seed=31))
+    ids = torch.from_numpy(rng.permuted(np.tile(np.arange(E), (T, 1)), axis=1)[:, :k].astype(np.int32)).cuda()
+    y, slots = c.w8a8_moe(x, sx, ids, gu, sgu, dn, sdn, out_dtype=torch.bfloat16)
+    offsets, rows, slots2 = c.cider_moe_plan(ids, E)
+    assert torch.equal(slots, slots2)
+    a = c.cider_w4a8_grouped_swiglu(x, sx, gu, sgu, offsets, row_index=rows, row_div=k, out_dtype=torch.bfloat16)
+    a_q, a_s = c.cider_quant_act(a, 0)
+    off = offsets.tolist()
+    for e in range(E):
+        lo, hi = off[e], off[e + 1]
+        if lo < hi:
+            part = [t[lo:hi].clone() for t in (a_q, a_s)]
+            o = c.cider_w4a8_gemm(*part, dn[e].clone(), sdn[e].clone(), out_dtype=torch.bfloat16)
+            assert torch.equal(y[lo:hi], o), e
+
+
+def test_two_streams_at_once():
+    """Blocks in flight together on two streams, each with its own outputs and workspaces: the results of either alone."""
+    c = cider()
+    E, I, H, k, T = 6, 96, 256, 3, 3500
+    gu, dn = moe_weights(E, I, H, 23)
+    nw = torch.ones(H, dtype=torch.bfloat16, device="cuda")
+    inputs, alone = [], []
+    for seed in (0, 1):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        x = torch.randn(T, H, generator=g, device="cuda").to(torch.bfloat16)
+        ids = torch.rand(T, E, generator=g, device="cuda").topk(k).indices.to(torch.int32)
+        inputs.append((x, ids, torch.rand(T, k, generator=g, device="cuda")))
+        alone.append([t.clone() for t in block(c, *inputs[-1], nw, gu, dn)])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(3):
+        for i in (0, 1):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(block(c, *inputs[i], nw, gu, dn))
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        for run in got[i]:
+            for a, b in zip(run, alone[i]):
+                assert torch.equal(a, b), i
+
+
+def test_captured_plan_with_a_workspace():
+    """Two captured plans of more ids than one launch takes, replayed by turns for new ids."""
+    c = cider()
+    T, k, E = 4000, 4, 50
+    need = c.cider_moe_plan_workspace_size(T, k, E)
+    assert need > 0
+    both = []
+    for _ in range(2):
+        ids = torch.zeros(T, k, dtype=torch.int32, device="cuda")
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        c.cider_moe_plan(ids, E, workspace=ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = c.cider_moe_plan(ids, E, workspace=ws)
+        both.append((ids, graph, out))
+    rng = np.random.default_rng(40)
+    for _ in range(3):
+        new = [rng.integers(-1, E, (T, k)).astype(np.int32) for _ in both]
+        for (ids, graph, _), n in zip(both, new):
+            ids.copy_(torch.from_numpy(n))
+            graph.replay()
+        torch.cuda.synchronize()
+        for (_, _, out), n in zip(both, new):
+            for a, o in zip(out, plain_plan(n, E)):
+                assert np.array_equal(a.cpu().numpy(), o)
+
+
+def test_repeats_are_bit_identical():
+    c = cider()
+    E, I, H, k, T = 6, 96, 256, 3, 900
+    gu, dn = moe_weights(E, I, H, 24)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn(T, H, generator=g, device="cuda").to(torch.bfloat16)
+    ids = torch.rand(T, E, generator=g, device="cuda").topk(k).indices.to(torch.int32)
+    w = torch.rand(T, k, generator=g, device="cuda")
+    nw = torch.ones(H, dtype=torch.bfloat16, device="cuda")
+    first = block(c, x, ids, w, nw, gu, dn)
+    for _ in range(20):
+        for a, b in zip(first, block(c, x, ids, w, nw, gu, dn)):
+            assert torch.equal(a, b)

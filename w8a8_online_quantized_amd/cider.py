@@ -540,8 +540,9 @@ def w4a8_linear(x, w_packed, w_scale, stream=None):
 
 # ---- expert blocks ----------------------------------------------------------
 # A decode step runs these on a few rows, where the call costs more than its
-# kernel: tensors that fit are passed with one test each, and pointers go to
-# ctypes as plain integers.
+# kernel: tensors that fit are passed with one test each, pointers go to
+# ctypes as plain integers, and outputs are made in the forms that torch parses
+# fastest (sizes as arguments 1.25 us, as a tuple 1.6, empty_like 1.1).
 
 def _need_on(dev, t, dtype, shape, name):
     """_need, and that the tensor lives on the current device `dev`, where the
@@ -568,6 +569,9 @@ def cider_moe_plan_workspace_size(T: int, top_k: int, n_experts: int) -> int:
     return n
 
 
+_plan_workspace_size = functools.lru_cache(maxsize=256)(cider_moe_plan_workspace_size)
+
+
 @_on_stream
 def cider_moe_plan(expert_ids, n_experts: int, offsets=None, rows=None, slots=None, workspace=None, stream=None):
     """int32 expert ids [T, top_k] (outside [0, n_experts): no expert) ->
@@ -576,7 +580,7 @@ def cider_moe_plan(expert_ids, n_experts: int, offsets=None, rows=None, slots=No
     dev = torch.cuda.current_device()
     T, top_k = shape = expert_ids.shape
     _need_on(dev, expert_ids, torch.int32, shape, "expert_ids")
-    need = cider_moe_plan_workspace_size(T, top_k, n_experts)
+    need = _plan_workspace_size(T, top_k, n_experts)
     if offsets is None:
         offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=expert_ids.device)
     else:
@@ -586,7 +590,7 @@ def cider_moe_plan(expert_ids, n_experts: int, offsets=None, rows=None, slots=No
     else:
         _need_on(dev, rows, torch.int32, (T * top_k,), "rows")
     if slots is None:
-        slots = torch.empty(shape, dtype=torch.int32, device=expert_ids.device)
+        slots = torch.empty_like(expert_ids)
     else:
         _need_on(dev, slots, torch.int32, shape, "slots")
     if need and workspace is None:
@@ -619,7 +623,7 @@ def _grouped(fn, gated, bits, x_q, x_scale, w, w_scale, offsets, row_index, row_
         raise ValueError("the gated product needs as many gate rows as up rows")
     n_out = N // 2 if gated else N
     if y is None:
-        y = torch.empty((P, n_out), dtype=out_dtype or torch.float16, device=x_q.device)
+        y = torch.empty(P, n_out, dtype=out_dtype or torch.float16, device=x_q.device)
     else:
         _need_on(dev, y, y.dtype, (P, n_out), "y")
     st = getattr(lib(), fn)(x_q.data_ptr(), x_scale.data_ptr(), x_rows, w.data_ptr(), w_scale.data_ptr(),
@@ -705,7 +709,7 @@ def cider_norm_quant(x=None, block=None, norm_weight=None, slots=None, weights=N
         _need_on(dev, block, t, (block_rows, K) if slots is not None else row, "block")
         pb = block.data_ptr()
         if h is None:
-            h = torch.empty(row, dtype=t, device=fp.device)
+            h = torch.empty(M, K, dtype=t, device=fp.device) if x is None else torch.empty_like(x)
     if post_weight is not None:
         _need_on(dev, post_weight, t, vec, "post_weight")
         pp = post_weight.data_ptr()
@@ -726,11 +730,11 @@ def cider_norm_quant(x=None, block=None, norm_weight=None, slots=None, weights=N
         pn = norm_weight.data_ptr()
         scales = _scale_shape(M, K, group_size)
         if x_q is None:
-            x_q = torch.empty(row, dtype=torch.int8, device=fp.device)
+            x_q = torch.empty(M, K, dtype=torch.int8, device=fp.device)
         else:
             _need_on(dev, x_q, torch.int8, row, "x_q")
         if x_scale is None:
-            x_scale = torch.empty(scales, dtype=torch.float32, device=fp.device)
+            x_scale = torch.empty(*scales, dtype=torch.float32, device=fp.device)
         else:
             _need_on(dev, x_scale, torch.float32, scales, "x_scale")
         pq, pc = x_q.data_ptr(), x_scale.data_ptr()
@@ -756,7 +760,7 @@ def cider_dequant_act(x_q, x_scale, group_size: int = 0, y=None, stream=None, ou
         raise ValueError("K must be a multiple of group_size")
     _need_on(dev, x_scale, torch.float32, _scale_shape(M, K, group_size), "x_scale")
     if y is None:
-        y = torch.empty(row, dtype=out_dtype or torch.float16, device=x_q.device)
+        y = torch.empty(M, K, dtype=out_dtype or torch.float16, device=x_q.device)
     else:
         _need_on(dev, y, y.dtype, row, "y")
     st = lib().cider_dequant_act(x_q.data_ptr(), x_scale.data_ptr(), M, K, group_size, y.data_ptr(), _fp_code(y, "y"),

@@ -135,9 +135,11 @@ __device__ __forceinline__ v4i unpack16(int lo, int hi) {
   return o;
 }
 
-// silu(g) * u of four outputs. exp and the reciprocal are the hardware's
-// (each within a few fp32 ulp): far below the 16-bit rounding that follows.
-// For g below -88 exp(-g) is infinite, its reciprocal 0 and the result -0.
+// silu(g) * u. exp is the hardware's 2^x on g * log2(e), whose rounding makes
+// its relative error grow as |g| * 2^-24 (5e-6 where exp reaches the end of
+// fp32); it and the reciprocal stay far below the 16-bit rounding that follows.
+// For g below -87.3 the reciprocal's value leaves the normal range and the
+// result may be -0 (the formula's is below 1.2e-36 * |u|).
 __device__ __forceinline__ float silu_mul(float g, float u) {
   return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
 }
