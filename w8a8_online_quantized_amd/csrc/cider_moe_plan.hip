@@ -16,8 +16,8 @@
 // launch up to kOneBlockIds ids; beyond, a first launch counts each block's
 // ids and a second one places them, every block summing the counts of the
 // blocks before it by itself. Kernel times (HIP events): 128 ids 3.5 us (an
-// empty launch), 4096 ids 6.1, 8192 ids 8.6 (7.7 in two launches), 262144 ids
-// 11.7 (3.1 MB; the scattered 4-byte stores and the two launches bound it).
+// empty launch), 4096 ids 6.0, 8192 ids 8.4 (7.7 in two launches), 262144 ids
+// 11.6 (3.1 MB; the scattered 4-byte stores and the two launches bound it).
 #include "cider_internal.h"
 
 namespace cider {
@@ -100,6 +100,7 @@ __global__ void __launch_bounds__(kThreads) plan_count(const int32_t* __restrict
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += kThreads) {
     int n = 0;
+#pragma unroll
     for (int w = 0; w < kWaves; ++w) n += cnt[w * E + e];
     ws[(int64_t)blockIdx.x * E + e] = n;
   }
@@ -151,6 +152,7 @@ __global__ void __launch_bounds__(kThreads) plan_place(const int32_t* __restrict
         total += part_total[p * E + e];
       }
     } else {
+#pragma unroll
       for (int w = 0; w < kWaves; ++w) total += cnt[w * E + e];
     }
   }
@@ -170,11 +172,13 @@ __global__ void __launch_bounds__(kThreads) plan_place(const int32_t* __restrict
   }
   if (e < E) {
     if (blockIdx.x == 0) offsets[e] = start;
-    int at = start + before;
-    for (int w = 0; w < kWaves; ++w) {   // counts become each wave's first place
-      const int n = cnt[w * E + e];
+    int at = start + before, n[kWaves];
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) n[w] = cnt[w * E + e];   // all in flight before the first is overwritten
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {                        // counts become each wave's first place
       cnt[w * E + e] = at;
-      at += n;
+      at += n[w];
     }
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) offsets[E] = kept;
