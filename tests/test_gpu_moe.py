@@ -299,6 +299,23 @@ def test_weights_past_4_gib_of_offsets():
     assert torch.equal(y, (2.0 * torch.arange(1, E + 1, device="cuda") + 5)[:, None].expand(E, N).to(torch.float16))
 
 
+@pytest.mark.parametrize("gated", [False, True])
+def test_rows_past_4_gib_of_offsets(gated):
+    """The last rows of 2.2 GB of codes and 4.6 GB of outputs are what they are alone."""
+    c = cider()
+    P, K, N = 1100000, 2048, 4200 if gated else 2100
+    g = torch.Generator(device="cuda").manual_seed(3)
+    codes = lambda *s: torch.randint(-127, 128, s, generator=g, device="cuda", dtype=torch.int8)  # noqa: E731
+    x = torch.zeros(P, K, dtype=torch.int8, device="cuda")
+    x[-700:] = codes(700, K)
+    sx, w, sw = torch.full((P,), 0.01, device="cuda"), codes(2, N, K), torch.full((2, N), 1e-4, device="cuda")
+    fn = c.cider_w8a8_grouped_swiglu if gated else c.cider_w8a8_grouped_gemm
+    y = fn(x, sx, w, sw, torch.tensor([0, P - 300, P], dtype=torch.int32, device="cuda"), out_dtype=torch.bfloat16)
+    o = fn(x[-700:].contiguous(), sx[:700], w, sw, torch.tensor([0, 400, 700], dtype=torch.int32, device="cuda"),
+           out_dtype=torch.bfloat16)
+    assert torch.equal(y[-700:], o) and not bool(y[:-700].any())
+
+
 def test_grouped_refuses_other_tensors():
     c = cider()
     x, sx, w, sw, off, idx = (t if t is None else t.cuda() for t in make([3, 4], 32, 64, 8, seed=11, T=5))

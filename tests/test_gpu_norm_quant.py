@@ -243,3 +243,28 @@ def test_norm_refuses_other_tensors():
         c.cider_norm_quant(x, x, nw, slots=torch.zeros(4, 65, dtype=torch.int32, device="cuda"),
                            weights=torch.zeros(4, 65, device="cuda"))
     assert np.prod(c.cider_norm_quant(x[:0], norm_weight=nw)[1].shape) == 0
+
+
+@pytest.mark.parametrize("M,K", [(600000, 4096), (150000, 16392), (600000, 4097)])
+def test_rows_past_32_bits_of_offsets(M, K):
+    """The last rows of more than 2^31 elements are what they are alone."""
+    c, t = cider(), torch.bfloat16
+    g = torch.Generator(device="cuda").manual_seed(K)
+    x = torch.zeros(M, K, dtype=t, device="cuda")
+    nw = rnd(g, K, t=t, mean=1.0, scale=0.2)
+    x[-5:] = rnd(g, 5, K, t=t)
+    tail = x[-5:].clone()
+    h, q, s = c.cider_norm_quant(x, x, nw, h=x)                      # in place: 2 x
+    y = c.cider_dequant_act(q, s, out_dtype=t)
+    h1, q1, s1 = c.cider_norm_quant(tail, tail, nw)
+    assert torch.equal(h[-5:], h1) and torch.equal(q[-5:], q1) and torch.equal(s[-5:], s1)
+    assert torch.equal(y[-5:], c.cider_dequant_act(q1, s1, out_dtype=t))
+    assert not bool(q[:7].any()) and not bool(s[:-5].any())
+    # expert rows from the same depth
+    slots = torch.tensor([[M - 1, M - 3], [M - 2, 0]], dtype=torch.int32, device="cuda")
+    near = torch.tensor([[4, 2], [3, 5]], dtype=torch.int32, device="cuda")   # row 5: none, as row 0 of x is zeros
+    w = torch.rand(2, 2, generator=g, device="cuda")
+    a = c.cider_norm_quant(None, h, nw, slots=slots, weights=w)
+    b = c.cider_norm_quant(None, h1, nw, slots=near, weights=w)
+    for i, j in zip(a, b):
+        assert torch.equal(i, j)
