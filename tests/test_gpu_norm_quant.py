@@ -133,6 +133,14 @@ def test_weighted_sum_of_expert_rows(M, K, k, dtype):
     assert bool(((h.double() - o).abs() <= o.abs() * half + err * (1 + half) + tiny).all())
 
 
+# more rows than are resident at once, where rows of some sizes share a workgroup
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("M,K", [(1025, 1024), (1027, 520), (1026, 2560), (1027, 2056), (1025, 512), (1030, 4096)])
+def test_many_rows(M, K, dtype):
+    test_residual_norm_and_codes(M, K, dtype)
+    test_weighted_sum_of_expert_rows(M, K, 3, dtype)
+
+
 @pytest.mark.parametrize("K", [96, 2048, 4000, 9000, 33])
 def test_norm_alone_and_in_place(K):
     c, t = cider(), torch.bfloat16

@@ -23,10 +23,11 @@
 // HBM-bound: each of x and the block's rows is read once, h and the codes are
 // written once. The row stays in registers from the first load to the codes.
 // Kernel times (HIP events): 4096 rows of 2560 fp16 with both norms and a gate
-// 17.8 us (73 MB, 4.1 TB/s), 4096 rows of 2048 bf16 each summing 8 expert rows
-// 37.1 us (177 MB, 4.8 TB/s; a plain copy reaches 5.1), one row 4.1 us (an empty
+// 16.5 us (73 MB, 4.5 TB/s), 4096 rows of 2048 bf16 each summing 8 expert rows
+// 31.2 us (177 MB, 5.7 TB/s; a plain copy reaches 5.1), one row 4.1 us (an empty
 // launch takes 3.5). Loads as address-space-1 vectors took these from 29.4
-// and 38.9 us: the compiler had made flat one-dword loads of them.
+// and 38.9 us to 17.8 and 37.1: the compiler had made flat one-dword loads of
+// them; past-the-cache loads and stores did the rest (load16_once).
 #include "cider_internal.h"
 #include "cider_quant_rule.h"
 
@@ -49,6 +50,19 @@ typedef __attribute__((address_space(1))) u4 global_u4;
 
 __device__ __forceinline__ u4 load16(const void* base, int64_t c) { return ((const global_u4*)base)[c]; }
 __device__ __forceinline__ void store16(void* base, int64_t c, u4 v) { ((global_u4*)base)[c] = v; }
+
+// The same past the caches' retention, for what is read or written once here:
+// a token's expert rows, and 16-bit rows whose reader comes a block later. The
+// inputs then stay in the last-level cache: 4096 rows of 4096 with both norms
+// 28.2 -> 21.4 us and, with the GEMM before it, 87.2 -> 83.5; expert rows
+// 36 -> 31. Not for x, a block in place, or the codes, which the next or last
+// launch also touches (codes: GEMM and norm of 4096 x 2560 45.4 -> 50.3).
+__device__ __forceinline__ u4 load16_once(const void* base, int64_t c) {
+  return __builtin_nontemporal_load((const global_u4*)base + c);
+}
+__device__ __forceinline__ void store16_once(void* base, int64_t c, u4 v) {
+  __builtin_nontemporal_store(v, (global_u4*)base + c);
+}
 
 // Eight values at once, as vectors: the conversions then come in pairs.
 typedef float f8 __attribute__((ext_vector_type(8)));
@@ -177,7 +191,13 @@ __global__ void __launch_bounds__(kThreads) norm_rows_reg(const NormArgs a) {
           w[j] = ok ? a.weights[at] : 0.0f;
 #pragma unroll
           for (int i = 0; i < CPL; ++i) v[j][i] = z;
-          if (ok) load_row(v[j], a.block, slot);
+          if (ok) {
+#pragma unroll
+            for (int i = 0; i < CPL; ++i) {
+              const int c = cl + kStride * i;
+              if (c < C) v[j][i] = load16_once(a.block, (int64_t)slot * C0 + c);
+            }
+          }
         }
 #pragma unroll
         for (int j = 0; j < kAhead; ++j)
@@ -238,7 +258,7 @@ __global__ void __launch_bounds__(kThreads) norm_rows_reg(const NormArgs a) {
 #pragma unroll
     for (int i = 0; i < CPL; ++i) {
       const int c = cl + kStride * i;
-      if (c < C) store16(a.h, row * C0 + c, hv[i]);
+      if (c < C) store16_once(a.h, row * C0 + c, hv[i]);
     }
   }
   if (!a.norm_weight) return;                    // uniform: the residual only
@@ -266,7 +286,7 @@ __global__ void __launch_bounds__(kThreads) norm_rows_reg(const NormArgs a) {
 #pragma unroll
     for (int i = 0; i < CPL; ++i) {
       const int c = cl + kStride * i;
-      if (c < C) store16(a.normed, row * C0 + c, pack8<BF>(t[i]));
+      if (c < C) store16_once(a.normed, row * C0 + c, pack8<BF>(t[i]));
     }
   }
   if (!a.x_q) return;
@@ -429,19 +449,24 @@ __global__ void __launch_bounds__(kThreads) norm_rows_loop(const NormArgs a) {
 
 template <bool BF>
 hipError_t launch_norm_t(const NormArgs& a, hipStream_t st) {
-  // Waves and chunks per row: as few as hold the row up to K = 1024, then four
-  // waves (4096 rows of K = 2048, one wave of 4 chunks per lane 19.5 us, two
-  // waves 13.3, four 13.0; one row 7.5 / 5.2 / 4.1), but two where four would
-  // leave most of their second chunks idle (K = 2560: four waves of 2 chunks
-  // 17.1 us, two of 3 16.5, one of 5 18.0).
+  // Waves and chunks per row. Up to four rows per CU every row is resident at
+  // once and its chain of latencies is the time: four waves, each with as few
+  // chunks as possible (256 rows of K = 1024 summing 8 expert rows: one wave
+  // of 2 chunks 6.4 us, four of 1 4.8; K = 2560 two of 3 8.8, four of 2 6.8;
+  // one row 6.1 / 5.2), except up to K = 512, which one wave of 1 holds. With more
+  // rows idle lanes cost: one wave up to K = 1024 (2048 rows 4.9 us, four waves
+  // 5.3), four at K = 2048 (4096 rows summing 8: 31.2 us, two waves 33.0, one 36.6),
+  // two where four would leave most of their second chunks idle (4096 rows of
+  // 2560 with both norms and a gate: 16.5 us, four waves 18.9, one 16.7).
   const dim3 block(kThreads);
   const unsigned rows1 = (unsigned)a.M, rows2 = (rows1 + 1) / 2, rows4 = (rows1 + 3) / 4;
   const int64_t C = a.K / 8;                     // 16-byte chunks per row
+  const bool few = a.M <= 4 * 256;
   if (a.K % 8 != 0) norm_rows_loop<1, BF><<<dim3(rows1), block, 0, st>>>(a);
   else if (C <= 64) norm_rows_reg<1, 1, BF><<<dim3(rows4), block, 0, st>>>(a);
-  else if (C <= 128) norm_rows_reg<2, 1, BF><<<dim3(rows4), block, 0, st>>>(a);
+  else if (C <= 128 && !few) norm_rows_reg<2, 1, BF><<<dim3(rows4), block, 0, st>>>(a);
   else if (C <= 256) norm_rows_reg<1, kWaves, BF><<<dim3(rows1), block, 0, st>>>(a);
-  else if (C <= 384) norm_rows_reg<3, 2, BF><<<dim3(rows2), block, 0, st>>>(a);
+  else if (C <= 384 && !few) norm_rows_reg<3, 2, BF><<<dim3(rows2), block, 0, st>>>(a);
   else if (C <= 512) norm_rows_reg<2, kWaves, BF><<<dim3(rows1), block, 0, st>>>(a);
   else if (C <= 768) norm_rows_reg<3, kWaves, BF><<<dim3(rows1), block, 0, st>>>(a);
   else if (C <= 1024) norm_rows_reg<4, kWaves, BF><<<dim3(rows1), block, 0, st>>>(a);
@@ -458,8 +483,8 @@ __device__ __forceinline__ float code_value(int8_t q, float s) {
   return v;
 }
 
-// y = fp(code * scale), 16 codes per thread when rows are whole 16-byte
-// chunks (K % 16 == 0; scale groups are multiples of 16), else one.
+// y = fp(code * scale), 8 codes per thread when rows are whole 8-byte chunks
+// (scale groups are multiples of 8), else one.
 template <int VEC, bool BF>
 __global__ void __launch_bounds__(kThreads) dequant_rows(const int8_t* __restrict__ q, const float* __restrict__ s,
                                                          int64_t M, int K, int group_size, uint16_t* __restrict__ y) {
@@ -470,17 +495,12 @@ __global__ void __launch_bounds__(kThreads) dequant_rows(const int8_t* __restric
     const int64_t row = i / per_row;
     const int c = (int)(i - row * per_row);
     const float sc = s[row * G + (group_size ? c * VEC / group_size : 0)];
-    if constexpr (VEC == 16) {
-      const uint4 v = reinterpret_cast<const uint4*>(q)[i];
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      float lo[8], hi[8];
+    if constexpr (VEC == 8) {
+      const uint2 v = reinterpret_cast<const uint2*>(q)[i];
+      float t[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        lo[e] = code_value((int8_t)(w[e >> 2] >> (8 * (e & 3))), sc);
-        hi[e] = code_value((int8_t)(w[2 + (e >> 2)] >> (8 * (e & 3))), sc);
-      }
-      store16(y, 2 * i, pack8<BF>(lo));
-      store16(y, 2 * i + 1, pack8<BF>(hi));
+      for (int e = 0; e < 8; ++e) t[e] = code_value((int8_t)((e < 4 ? v.x : v.y) >> (8 * (e & 3))), sc);
+      store16_once(y, i, pack8<BF>(t));
     } else {
       y[i] = round16<BF>(code_value(q[i], sc));
     }
@@ -490,11 +510,11 @@ __global__ void __launch_bounds__(kThreads) dequant_rows(const int8_t* __restric
 template <bool BF>
 hipError_t launch_dequant_t(const int8_t* q, const float* s, int64_t M, int64_t K, int group_size, void* y,
                             hipStream_t st) {
-  const bool vec = K % 16 == 0;
-  const int64_t items = M * (vec ? K / 16 : K);
+  const bool vec = K % 8 == 0;
+  const int64_t items = M * (vec ? K / 8 : K);
   const unsigned blocks = (unsigned)((items + kThreads - 1) / kThreads < 16384 ? (items + kThreads - 1) / kThreads : 16384);
   if (vec)
-    dequant_rows<16, BF><<<dim3(blocks), dim3(kThreads), 0, st>>>(q, s, M, (int)K, group_size, static_cast<uint16_t*>(y));
+    dequant_rows<8, BF><<<dim3(blocks), dim3(kThreads), 0, st>>>(q, s, M, (int)K, group_size, static_cast<uint16_t*>(y));
   else
     dequant_rows<1, BF><<<dim3(blocks), dim3(kThreads), 0, st>>>(q, s, M, (int)K, group_size, static_cast<uint16_t*>(y));
   return hipGetLastError();
