@@ -56,7 +56,7 @@ __device__ __forceinline__ void store16(void* base, int64_t c, u4 v) { ((global_
 // inputs then stay in the last-level cache: 4096 rows of 4096 with both norms
 // 28.2 -> 21.4 us and, with the GEMM before it, 87.2 -> 83.5; expert rows
 // 36 -> 31. Not for x, a block in place, or the codes, which the next or last
-// launch also touches (codes: GEMM and norm of 4096 x 2560 45.4 -> 50.3).
+// launch also touches (codes: GEMM and norm of 4096 x 2560 45.4 -> 49.4).
 __device__ __forceinline__ u4 load16_once(const void* base, int64_t c) {
   return __builtin_nontemporal_load((const global_u4*)base + c);
 }
