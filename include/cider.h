@@ -412,6 +412,9 @@ cider_status_t cider_stack_forward_dt(const void* x, int32_t dtype, int64_t M, i
 /* Most experts of one call, and most choices of one token (cider_norm_quant). */
 #define CIDER_MOE_MAX_EXPERTS 512
 #define CIDER_MOE_MAX_TOP_K 64
+/* Largest K of the grouped products with packed int4 weights: they sum
+ * 16 * code, and 16 * 128 * 8 * K < 2^31 holds every int8 code times every nibble. */
+#define CIDER_MOE_MAX_K_PACKED 131040
 
 /* Routing plan: the stable sort of P = T * top_k expert ids.
  *   expert_ids : int32 [T, top_k]; an id outside [0, n_experts) belongs to no
@@ -452,8 +455,8 @@ cider_status_t cider_moe_plan(const int32_t* expert_ids, int64_t T, int32_t top_
  *               or >= x_rows gives zeros. Without it x_rows must be >= P.
  *   y         : fp16 or bf16 [P, N] (y_dtype); rows from offsets[n_experts]
  *               on are left as they were.
- * K a multiple of 16 (32 for packed weights), any N; one expert's weights
- * must be below 2^31 bytes and, with row_index, so must x_q; 1 <= row_div;
+ * K a multiple of 16 (32 for packed weights, and at most
+ * CIDER_MOE_MAX_K_PACKED), any N; one expert's weights must be below 2^31 bytes and, with row_index, so must x_q; 1 <= row_div;
  * 1 <= n_experts <= CIDER_MOE_MAX_EXPERTS; P, x_rows < 2^31. (P, N) whose
  * output tiles would take 2^31 GPU threads return CIDER_ERROR_INVALID_VALUE.
  * P == 0 or N == 0 does nothing. Other errors as for cider_w8a8_gemm. */

@@ -120,3 +120,15 @@ def test_dequant_rejects(L):
     assert d(P, P, 4, 64, 0, NULL, 0, NULL) == INV and d(MIS, P, 4, 64, 0, P, 0, NULL) == INV
     assert d(P, P, 4, 64, 0, MIS, 0, NULL) == INV
     assert d(NULL, NULL, 0, 64, 0, NULL, 0, NULL) == 0
+
+
+@pytest.mark.parametrize("name", GROUPED)
+def test_packed_sums_bound_k(L, name):
+    """The packed products sum 16 * code: K beyond the exact sums of every code is refused, int8 weights take MAX_K."""
+    def call(K):                                                            # no rows: nothing is launched
+        return getattr(L, name)(P, P, 0, P, P, P, NULL, 1, 0, 64, K, 4, P, 0, NULL)
+    with open(cider.HEADER_PATH) as f:
+        most = int(f.read().split("CIDER_MOE_MAX_K_PACKED ")[1].split()[0])
+    assert most % 32 == 0 and 16 * 128 * 8 * most < 1 << 31 <= 16 * 128 * 8 * (most + 32)
+    i4 = "w4a8" in name
+    assert call(most) == 0 and call(most + 32) == (INV if i4 else 0) and call(MAX_K) == (INV if i4 else 0)

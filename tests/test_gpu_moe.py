@@ -547,3 +547,23 @@ def test_repeats_are_bit_identical():
     for _ in range(20):
         for a, b in zip(first, block(c, x, ids, w, nw, gu, dn)):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("n", [2, 70])
+def test_packed_sums_of_the_largest_codes(n):
+    """The longest K of packed weights with every code at its end (-128 and 127 times nibbles 0 and 15): exact, as the
+    dense entry's."""
+    c = cider()
+    K, N = 131040, 48
+    x = torch.full((n, K), -128, dtype=torch.int8, device="cuda")
+    x[1::2] = 127
+    w = torch.zeros(1, N, K // 2, dtype=torch.uint8, device="cuda")
+    w[:, 1::2] = 255
+    sx, sw = torch.full((n,), 2.0 ** -12, device="cuda"), torch.ones(1, N, device="cuda")
+    y = c.cider_w4a8_grouped_gemm(x, sx, w, sw, torch.tensor([0, n], dtype=torch.int32, device="cuda"))
+    v = (x[:, :1].double() * torch.tensor([-8.0, 7.0], device="cuda").repeat(N // 2) * K).to(torch.float32)
+    assert torch.equal(y, (v * 2.0 ** -12).to(torch.float16))
+    assert torch.equal(y, c.cider_w4a8_gemm(x, sx, w[0], sw[0]))
+    with pytest.raises(c.CiderError):
+        c.cider_w4a8_grouped_gemm(torch.cat((x, x[:, :32]), 1), sx, torch.cat((w, w[..., :16]), 2), sw,
+                                  torch.tensor([0, n], dtype=torch.int32, device="cuda"))

@@ -649,7 +649,7 @@ def cider_w8a8_grouped_gemm(x_q, x_scale, w_q, w_scale, offsets, row_index=None,
 @_on_stream
 def cider_w4a8_grouped_gemm(x_q, x_scale, w_packed, w_scale, offsets, row_index=None, row_div: int = 1, y=None,
                             stream=None, out_dtype=None):
-    """cider_w8a8_grouped_gemm with packed int4 weights [E, N, K / 2]."""
+    """cider_w8a8_grouped_gemm with packed int4 weights [E, N, K / 2], K below 131072."""
     return _grouped("cider_w4a8_grouped_gemm", False, 4, x_q, x_scale, w_packed, w_scale, offsets, row_index, row_div,
                     y, stream, out_dtype)
 
@@ -666,7 +666,7 @@ def cider_w8a8_grouped_swiglu(x_q, x_scale, w_q, w_scale, offsets, row_index=Non
 @_on_stream
 def cider_w4a8_grouped_swiglu(x_q, x_scale, w_packed, w_scale, offsets, row_index=None, row_div: int = 1, y=None,
                               stream=None, out_dtype=None):
-    """cider_w8a8_grouped_swiglu with packed int4 weights [E, N, K / 2]."""
+    """cider_w8a8_grouped_swiglu with packed int4 weights [E, N, K / 2], K below 131072."""
     return _grouped("cider_w4a8_grouped_swiglu", True, 4, x_q, x_scale, w_packed, w_scale, offsets, row_index, row_div,
                     y, stream, out_dtype)
 

@@ -613,6 +613,7 @@ static cider_status_t grouped_common(const int8_t* x_q, const float* x_scale, in
   const bool i4 = wk == cider::kWeightI4;
   constexpr int64_t kLimit = int64_t(1) << 31;
   if (!valid_dtype(y_dtype) || !gemm_sizes_ok(P, N) || !valid_k(K, i4 ? 32 : 16, 0)) return CIDER_ERROR_INVALID_VALUE;
+  if (i4 && K > CIDER_MOE_MAX_K_PACKED) return CIDER_ERROR_INVALID_VALUE;   // their sums are of 16 * code
   if (x_rows < 0 || x_rows >= kLimit || row_div < 1 || n_experts < 1 || n_experts > CIDER_MOE_MAX_EXPERTS ||
       (gated && N % 2 != 0))
     return CIDER_ERROR_INVALID_VALUE;

@@ -124,8 +124,8 @@ __device__ __forceinline__ Unit find_unit(const int32_t* __restrict__ offsets, i
 // order 0,2,4,6 | 1,3,5,7 | 8,10,12,14 | 9,11,13,15: a nibble in a byte's upper
 // half with its top bit flipped is 16 * (nibble - 8) in two's complement, two
 // or three operations for four codes where sign-extending them takes five. The
-// sums stay exact, 16 * 127 * 7 * CIDER_MAX_K < 2^31, and are shifted back once
-// at the end.
+// sums stay exact for every code and nibble, 16 * 128 * 8 * K < 2^31 up to
+// CIDER_MOE_MAX_K_PACKED, and are shifted back once at the end.
 __device__ __forceinline__ v4i unpack16(int lo, int hi) {
   v4i o;
   o.x = (int)((((uint32_t)lo << 4) & 0xF0F0F0F0u) ^ 0x80808080u);
@@ -167,6 +167,7 @@ grouped_kernel(const GroupedArgs g) {
   constexpr int kPadBytes = kPad ? 1024 : 0;
   constexpr int BNO = GATED ? BN / 2 : BN;               // output columns per tile
   constexpr int TNO = GATED ? TN / 2 : TN;               // 16-column output fragments per wave
+  static_assert(int64_t(16) * 128 * 8 * CIDER_MOE_MAX_K_PACKED < (int64_t(1) << 31), "int4 sums");
   static_assert(TM * 16 == WTM && TN * 16 == WTN && (!GATED || TN % 2 == 0), "wave tile");
   static_assert(BM * RBA % 1024 == 0 && BN * RBW % 1024 == 0, "whole DMA blocks");
   static_assert((NW * (1024 / RBA)) % 16 == 0 && (NW * (1024 / RBW)) % 16 == 0, "a wave's blocks share a swizzle slot");
