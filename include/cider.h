@@ -509,8 +509,10 @@ cider_status_t cider_w4a8_grouped_swiglu(const int8_t* x_q, const float* x_scale
  * in place); no other buffers may overlap. x_q and x_scale go together; they
  * and normed need norm_weight. alpha finite, eps positive and finite, 1 <=
  * top_k <= CIDER_MOE_MAX_TOP_K with slots, M < 2^23, 1 <= K <= CIDER_MAX_K,
- * K % group_size == 0. Values whose squares overflow fp32 are unspecified, as
- * are non-finite ones. */
+ * K % group_size == 0. A row of h that holds a non-finite value, or whose
+ * squares overflow fp32, has NaN in normed and in all of its scales, and codes
+ * 0; such a row of p before a post_weight gives a row of NaN in h. A NaN in
+ * norm_weight gives NaN in every scale that it enters. */
 typedef struct {
   const void* x;
   const void* block;

@@ -276,3 +276,40 @@ def test_rows_past_32_bits_of_offsets(M, K):
     b = c.cider_norm_quant(None, h1, nw, slots=near, weights=w)
     for i, j in zip(a, b):
         assert torch.equal(i, j)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("M,K", [(9, 512), (9, 2048), (9, 2112), (9, 8192), (9, 9088), (9, 77), (1030, 1024), (1031, 2560)])
+def test_rows_that_overflow_do_not_vanish(M, K, dtype):
+    """A residual that is not finite, or whose squares overflow fp32, gives NaN scales and normed rows in every form;
+    the rows beside it are what they are without it."""
+    c, t = cider(), DT[dtype]
+    g = torch.Generator(device="cuda").manual_seed(K)
+    x, block, nw = rnd(g, M, K, t=t), rnd(g, M, K, t=t), rnd(g, K, t=t, mean=1.0, scale=0.2)
+    bad = {1: float("nan"), 3: float("inf"), 4: float("-inf"), M - 2: 60000.0 if dtype == "fp16" else 3e30}
+    wild, wild_block = x.clone(), block.clone()
+    for row, v in bad.items():
+        wild[row, K // 3] = v
+    wild_block[M - 2, K // 3] = bad[M - 2]                             # 120000 in fp16; 3.6e61 squared in bf16
+    hit = torch.zeros(M, dtype=torch.bool, device="cuda")
+    hit[list(bad)] = True
+    for gs in (0, 64, 128):
+        if gs and K % gs:
+            continue
+        n0, n1 = torch.empty_like(x), torch.empty_like(x)
+        a = c.cider_norm_quant(x, block, nw, group_size=gs, normed=n0)
+        b = c.cider_norm_quant(wild, wild_block, nw, group_size=gs, normed=n1)
+        assert bool(b[2][hit].isnan().all()) and bool(n1[hit].isnan().all()) and not bool(b[1][hit].any()), gs
+        assert bool(c.cider_dequant_act(b[1], b[2], gs)[hit].isnan().all())
+        for i, j in zip((*a, n0), (*b, n1)):
+            assert torch.equal(i[~hit], j[~hit]), gs
+        # in the block alone, before its own norm: the residual's row is NaN
+        h, q, s = c.cider_norm_quant(x, wild if dtype == "bf16" else torch.where(hit[:, None], wild * 2, wild), nw,
+                                     post_weight=nw, group_size=gs)
+        assert bool(h[hit].isnan().all()) and bool(s[hit].isnan().all()) and not bool(q[hit].any())
+        assert bool(h[~hit].isfinite().all()) and bool(s[~hit].isfinite().all())
+        # a weight that is NaN reaches the scales it enters
+        lost = nw.clone()
+        lost[K - 1] = float("nan")
+        _, _, s = c.cider_norm_quant(x, block, lost, group_size=gs)
+        assert bool((s.view(M, -1)[:, -1]).isnan().all()) and bool((s.view(M, -1)[:, :-1]).isfinite().all())

@@ -100,7 +100,7 @@ __device__ __forceinline__ float wave_sum(float v) {
 
 __device__ __forceinline__ float wave_max(float v) {
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v = __builtin_fmaxf(v, __shfl_xor(v, off));
+  for (int off = 32; off >= 1; off >>= 1) v = __builtin_elementwise_maximum(v, __shfl_xor(v, off));
   return v;
 }
 
@@ -122,13 +122,17 @@ __device__ __forceinline__ void row_reduce(float& sum, float& mx, float* red, in
 #pragma unroll
     for (int w = 1; w < WPR; ++w) {
       sum += red[w0 + w];
-      mx = __builtin_fmaxf(mx, red[kWaves + w0 + w]);
+      mx = __builtin_elementwise_maximum(mx, red[kWaves + w0 + w]);
     }
   }
 }
 
+// NaN for a row that is not finite or whose squares overflow: 1 / sqrt(inf)
+// would turn its finite values into zeros. With it, and maxima that keep a NaN
+// (v_maximum3_f32), every scale of the row is NaN, per row or per group.
 __device__ __forceinline__ float inv_rms(float sum, int64_t K, float eps) {
-  return 1.0f / __builtin_sqrtf(sum / (float)K + eps);
+  const float v = sum / (float)K + eps;
+  return __builtin_isfinite(v) ? 1.0f / __builtin_sqrtf(v) : __builtin_nanf("");
 }
 
 // Rows of K % 8 == 0 that fit the registers of WPR waves (4 / WPR rows per
@@ -273,7 +277,7 @@ __global__ void __launch_bounds__(kThreads) norm_rows_reg(const NormArgs a) {
     for (int e = 0; e < 8; ++e) {                // chunks past the row are zeros
       sum = __builtin_fmaf(h[e], h[e], sum);
       t[i][e] = h[e] * w[e];
-      mx = __builtin_fmaxf(mx, __builtin_fabsf(t[i][e]));
+      mx = __builtin_elementwise_maximum(mx, __builtin_fabsf(t[i][e]));
     }
   }
   row_reduce<WPR>(sum, mx, red[1], wave, lane);
@@ -300,15 +304,15 @@ __global__ void __launch_bounds__(kThreads) norm_rows_reg(const NormArgs a) {
     if (lpg) {
       float m = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) m = __builtin_fmaxf(m, __builtin_fabsf(t[i][e]));
+      for (int e = 0; e < 8; ++e) m = __builtin_elementwise_maximum(m, __builtin_fabsf(t[i][e]));
 #pragma unroll
-      for (int off = 4; off >= 1; off >>= 1) m = __builtin_fmaxf(m, __shfl_xor(m, off));
-      const float m16 = __builtin_fmaxf(m, __shfl_xor(m, 8));
+      for (int off = 4; off >= 1; off >>= 1) m = __builtin_elementwise_maximum(m, __shfl_xor(m, off));
+      const float m16 = __builtin_elementwise_maximum(m, __shfl_xor(m, 8));
       s = (lpg == 16 ? m16 : m) / 127.0f;
       if ((lane & (lpg - 1)) == 0 && c < C) a.x_scale[row * (C0 / lpg) + c / lpg] = s;
     }
     if (c < C) {
-      const uint2 q = s != 0.0f ? code_bytes_of_values<false>(t[i], s, 1.0f / s, 127.0f) : make_uint2(0, 0);
+      const uint2 q = s > 0.0f ? code_bytes_of_values<false>(t[i], s, 1.0f / s, 127.0f) : make_uint2(0, 0);
       *reinterpret_cast<uint2*>(a.x_q + row * a.K + (int64_t)c * 8) = q;
     }
   }
@@ -395,7 +399,7 @@ __global__ void __launch_bounds__(kThreads) norm_rows_loop(const NormArgs a) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         sum = __builtin_fmaf(h[e], h[e], sum);
-        mx = __builtin_fmaxf(mx, __builtin_fabsf(h[e] * w[e]));
+        mx = __builtin_elementwise_maximum(mx, __builtin_fabsf(h[e] * w[e]));
       }
     }
   }
@@ -427,19 +431,19 @@ __global__ void __launch_bounds__(kThreads) norm_rows_loop(const NormArgs a) {
       if (lpg) {
         float m = 0.0f;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) m = __builtin_fmaxf(m, __builtin_fabsf(t[e]));
+        for (int e = 0; e < VEC; ++e) m = __builtin_elementwise_maximum(m, __builtin_fabsf(t[e]));
 #pragma unroll
-        for (int off = 4; off >= 1; off >>= 1) m = __builtin_fmaxf(m, __shfl_xor(m, off));
-        const float m16 = __builtin_fmaxf(m, __shfl_xor(m, 8));
+        for (int off = 4; off >= 1; off >>= 1) m = __builtin_elementwise_maximum(m, __shfl_xor(m, off));
+        const float m16 = __builtin_elementwise_maximum(m, __shfl_xor(m, 8));
         s = (lpg == 16 ? m16 : m) / 127.0f;
         if (in && (lane & (lpg - 1)) == 0) a.x_scale[row * (K / a.group_size) + k / a.group_size] = s;
       }
       if (in)
         *reinterpret_cast<uint2*>(a.x_q + row * K + k) =
-            s != 0.0f ? code_bytes_of_values<false>(t, s, 1.0f / s, 127.0f) : make_uint2(0, 0);
+            s > 0.0f ? code_bytes_of_values<false>(t, s, 1.0f / s, 127.0f) : make_uint2(0, 0);
     } else {
       if (in) {
-        float q = s != 0.0f ? __builtin_rintf(t[0] / s) : 0.0f;
+        float q = s > 0.0f ? __builtin_rintf(t[0] / s) : 0.0f;
         q = __builtin_fminf(__builtin_fmaxf(q, -127.0f), 127.0f);
         a.x_q[row * K + k] = (int8_t)q;
       }
