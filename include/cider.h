@@ -526,7 +526,7 @@ typedef struct {
   int8_t* x_q;
   float* x_scale;
   int64_t M, K;
-  int64_t block_rows;    /* rows of block, with slots */
+  int64_t block_rows;    /* rows of block, with slots; 0: block is not read, but must not be NULL */
   int64_t rows_per_gate; /* 0: one gate row */
   int32_t dtype;         /* a cider_dtype_t */
   int32_t top_k;

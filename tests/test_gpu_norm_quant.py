@@ -313,3 +313,20 @@ def test_rows_that_overflow_do_not_vanish(M, K, dtype):
         lost[K - 1] = float("nan")
         _, _, s = c.cider_norm_quant(x, block, lost, group_size=gs)
         assert bool((s.view(M, -1)[:, -1]).isnan().all()) and bool((s.view(M, -1)[:, :-1]).isfinite().all())
+
+
+@pytest.mark.parametrize("M,K", [(0, 64), (1, 64), (3, 77), (2, 9000)])
+def test_no_expert_rows_at_all(M, K):
+    """A rank whose experts got no token: an empty block adds nothing to any row."""
+    c, t = cider(), torch.bfloat16
+    g = torch.Generator(device="cuda").manual_seed(K)
+    x, nw = rnd(g, M, K, t=t), rnd(g, K, t=t, mean=1.0, scale=0.2)
+    block = torch.empty(0, K, dtype=t, device="cuda")
+    slots, w = torch.full((M, 2), -1, dtype=torch.int32, device="cuda"), torch.ones(M, 2, device="cuda")
+    for kw in (dict(), dict(post_weight=nw)):
+        h, q, s = c.cider_norm_quant(x, block, nw, slots=slots, weights=w, **kw)
+        assert torch.equal(h, x)
+        for a, b in zip((q, s), c.cider_norm_quant(x, norm_weight=nw)[1:]):
+            assert torch.equal(a, b)
+    h, _, _ = c.cider_norm_quant(None, block, slots=slots, weights=w)
+    assert h.shape == (M, K) and not bool(h.any())

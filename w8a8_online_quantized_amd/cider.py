@@ -722,6 +722,8 @@ def cider_norm_quant(x=None, block=None, norm_weight=None, slots=None, weights=N
     if h is not None:
         _need_on(dev, h, t, row, "h")
         ph = h.data_ptr()
+        if slots is not None and not block_rows:
+            pb = ph                                 # no expert rows: nothing is read, and an empty tensor has no pointer
     if normed is not None:
         _need_on(dev, normed, t, row, "normed")
         pd = normed.data_ptr()
