@@ -567,3 +567,19 @@ def test_packed_sums_of_the_largest_codes(n):
     with pytest.raises(c.CiderError):
         c.cider_w4a8_grouped_gemm(torch.cat((x, x[:, :32]), 1), sx, torch.cat((w, w[..., :16]), 2), sw,
                                   torch.tensor([0, n], dtype=torch.int32, device="cuda"))
+
+
+@pytest.mark.parametrize("P,E,share", [(800001, 40, 2048), (1100001, 299, 4096), (2500003, 7, 8192), (2300001, 512, 8192),
+                                       (9001, 1, 0)])
+def test_plan_of_grown_chunks(P, E, share):
+    """More ids than the largest grid has usual chunks for: blocks take more than `share` ids each (asserted by the
+    workspace, so that another choice of chunks cannot pass this by). Beyond 8192 a wave walks its ids in several
+    rounds, the last of them partial."""
+    c = cider()
+    blocks = c.cider_moe_plan_workspace_size(P, 1, E) // (4 * E)
+    assert blocks > 1 and blocks * share < P
+    rng = np.random.default_rng(P)
+    ids = rng.integers(-1, E + 1, (P, 1)).astype(np.int32)
+    check_plan(c, ids, E)
+    ids[:] = np.sort(ids, 0)                                       # whole chunks of one expert, all dropped ids at the ends
+    check_plan(c, ids, E)
