@@ -583,3 +583,63 @@ def test_plan_of_grown_chunks(P, E, share):
     check_plan(c, ids, E)
     ids[:] = np.sort(ids, 0)                                       # whole chunks of one expert, all dropped ids at the ends
     check_plan(c, ids, E)
+
+
+# Launches of the larger tiles again, in every type: by the rule of tiles the plain
+# products take 128 x 256, 128 x 256, 256 x 192 and 256 x 256 (rows by columns), the
+# gated ones 256 x 192, 256 x 256, 256 x 256 and 128 x 256.
+LARGE = [([1399, 3, 1598], 5003, 160), ([1300, 1200], 2500, 96), ([2300, 200], 8008, 128), ([2000, 0, 2000], 6000, 288)]
+
+
+def gated_off(y, v, dtype):
+    """How far gated rows are outside assert_gated's bound, on the GPU."""
+    n = v.shape[1] // 2
+    g, u = v[:, :n].double(), v[:, n:].double()
+    o = g * torch.sigmoid(g) * u
+    half = torch.finfo(dtype).eps / 2
+    tiny = torch.finfo(dtype).tiny * torch.finfo(dtype).eps / 2
+    bound = o.abs() * (half + (8 + g.abs()) * 2.0 ** -23 * (1 + half)) + tiny + u.abs() * 2.0 ** -118
+    return float(((y.double() - o).abs() - bound).max())
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("counts,N,K", LARGE)
+def test_large_tiles(counts, N, K, gated, bits, dtype):
+    """In place and gathered, with sources out of range, and rows behind the last group left as they were."""
+    c, t = cider(), DT[dtype]
+    n = 2 * N if gated else N
+    for T in (None, 500):
+        x, sx, w, sw, off, idx = (v if v is None else v.cuda() for v in make(counts, n, K, bits, seed=N, T=T, k=2))
+        P = int(off[-1])
+        bad = torch.zeros(P, dtype=torch.bool, device="cuda")
+        if idx is None:
+            x, sx = torch.cat((x, x[:7])), torch.cat((sx, sx[:7]))
+        else:
+            idx[::3], idx[1::5], idx[2::7] = -1, 1000, 2 ** 31 - 1   # 1000 // 2: past the last row
+            bad = (idx < 0) | (idx >= 1000)
+            idx = torch.cat((idx, idx[:7]))
+        y = torch.full((P + 7, N), 7.5, dtype=t, device="cuda")
+        call(c, bits, gated, x, sx, w, sw, off, idx, 2, y=y)
+        v = plain_values(x, sx, w, sw, off.cpu(), None if idx is None else torch.where(bad, 0, idx[:P]), 2, bits)
+        v[bad] = 0.0
+        assert bool((y[P:] == 7.5).all()) and not bool(y[:P][bad].any())
+        if gated:
+            assert gated_off(y[:P], v, t) <= 0, T
+        else:
+            assert torch.equal(y[:P].view(torch.int16), v.to(t).view(torch.int16)), T
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_large_tiles_of_offsets_out_of_order(gated):
+    """Clamped, whatever they hold; rows past P are never written."""
+    c = cider()
+    n, N, K = 2000, 6000, 96
+    x, sx, w, sw, _, _ = (v if v is None else v.cuda() for v in make([n, n], 2 * N if gated else N, K, 8, seed=9))
+    back = torch.full((2 * n + 2, N), 3.0, dtype=torch.float16, device="cuda")
+    fn = c.cider_w8a8_grouped_swiglu if gated else c.cider_w8a8_grouped_gemm
+    for off in ([0, 5 * n, 2 * n], [-7, n, 10 ** 9], [2 ** 31 - 1, 0, -2 ** 31], [n + 10, 20, 2 * n], [0, 0, 0]):
+        fn(x, sx, w, sw, torch.tensor(off, dtype=torch.int64).to(torch.int32).cuda(), y=back[:2 * n])
+        torch.cuda.synchronize()
+        assert bool((back[2 * n:] == 3.0).all())
