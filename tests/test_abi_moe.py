@@ -132,3 +132,11 @@ def test_packed_sums_bound_k(L, name):
     assert most % 32 == 0 and 16 * 128 * 8 * most < 1 << 31 <= 16 * 128 * 8 * (most + 32)
     i4 = "w4a8" in name
     assert call(most) == 0 and call(most + 32) == (INV if i4 else 0) and call(MAX_K) == (INV if i4 else 0)
+
+
+def test_workspaces_are_device_memory():
+    """A workspace on the host is refused before its pointer reaches a kernel."""
+    torch = pytest.importorskip("torch")
+    assert cider._ws_args(None) == (None, 0)
+    with pytest.raises(TypeError):
+        cider._ws_args(torch.empty(1 << 16, dtype=torch.uint8))

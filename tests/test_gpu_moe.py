@@ -643,3 +643,17 @@ def test_large_tiles_of_offsets_out_of_order(gated):
         fn(x, sx, w, sw, torch.tensor(off, dtype=torch.int64).to(torch.int32).cuda(), y=back[:2 * n])
         torch.cuda.synchronize()
         assert bool((back[2 * n:] == 3.0).all())
+
+
+def test_plan_refuses_other_workspaces():
+    c = cider()
+    ids = torch.zeros(3000, 4, dtype=torch.int32, device="cuda")
+    need = c.cider_moe_plan_workspace_size(3000, 4, 9)
+    with pytest.raises(TypeError):
+        c.cider_moe_plan(ids, 9, workspace=torch.empty(need, dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        c.cider_moe_plan(ids, 9, workspace=torch.empty(2 * need, dtype=torch.uint8, device="cuda")[::2])
+    with pytest.raises(c.CiderError):
+        c.cider_moe_plan(ids, 9, workspace=torch.empty(need - 16, dtype=torch.uint8, device="cuda"))
+    wide = torch.empty(need // 4, dtype=torch.int32, device="cuda")  # any element type
+    assert int(c.cider_moe_plan(ids, 9, workspace=wide)[0][1]) == 12000

@@ -300,8 +300,14 @@ def cider_gemm_workspace_size(M: int, N: int, K: int, bits: int = 8, group_size:
 
 
 def _ws_args(workspace):
+    """Pointer and bytes of a workspace, which kernels write: it must be device
+    memory, and its bytes one range."""
     if workspace is None:
         return None, 0
+    if not workspace.is_cuda:
+        raise TypeError("workspace must be a CUDA (HIP) tensor")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     return _ptr(workspace), workspace.numel() * workspace.element_size()
 
 
@@ -437,8 +443,7 @@ def cider_linear(x, w, w_scale, bits: int = 8, group_size: int = 0, workspace=No
     if y is None:
         y = torch.empty((M, N), dtype=x.dtype, device=x.device)
     _need(y, x.dtype, (M, N), "y")
-    wsp = _ptr(workspace) if workspace is not None else None
-    wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    wsp, wsb = _ws_args(workspace)
     _check("cider_linear_dt", lib().cider_linear_dt(_ptr(x), dt, _ptr(w), _ptr(w_scale), M, N, K, bits, group_size,
                                                     wsp, wsb, _ptr(y), _stream(stream)))
     return y
@@ -595,6 +600,8 @@ def cider_moe_plan(expert_ids, n_experts: int, offsets=None, rows=None, slots=No
         _need_on(dev, slots, torch.int32, shape, "slots")
     if need and workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=expert_ids.device)
+    elif workspace is not None and workspace.is_cuda and workspace.get_device() != dev:
+        raise ValueError(f"workspace must be on the current device {dev}, not {workspace.get_device()}")
     st = lib().cider_moe_plan(expert_ids.data_ptr(), T, top_k, n_experts, offsets.data_ptr(), rows.data_ptr(),
                               slots.data_ptr(), *_ws_args(workspace), _raw_stream(stream, dev))
     if st:
@@ -847,5 +854,5 @@ def cider_stack_forward(x, layers, dims, workspace=None, y=None, stream=None):
             arr[i].s[j] = ws.data_ptr()
     _check("cider_stack_forward_dt", lib().cider_stack_forward_dt(
         _ptr(x), dt, M, hidden, q_dim, kv_dim, mlp_dim, len(layers), ctypes.cast(arr, ctypes.c_void_p),
-        _ptr(workspace), workspace.numel(), _ptr(y), _stream(stream)))
+        *_ws_args(workspace), _ptr(y), _stream(stream)))
     return y, workspace
