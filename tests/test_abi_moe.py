@@ -140,3 +140,10 @@ def test_workspaces_are_device_memory():
     assert cider._ws_args(None) == (None, 0)
     with pytest.raises(TypeError):
         cider._ws_args(torch.empty(1 << 16, dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("k,E", [(1, (1 << 32) + 8), ((1 << 32) + 1, 8), (1, 1 << 31), (1, -(1 << 32) + 8)])
+def test_sizes_past_32_bits_are_refused(k, E):
+    """ctypes takes an int32 argument modulo 2^32: such sizes must not pass for small ones."""
+    with pytest.raises(ValueError):
+        cider.cider_moe_plan_workspace_size(4, k, E)

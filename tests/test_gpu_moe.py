@@ -657,3 +657,16 @@ def test_plan_refuses_other_workspaces():
         c.cider_moe_plan(ids, 9, workspace=torch.empty(need - 16, dtype=torch.uint8, device="cuda"))
     wide = torch.empty(need // 4, dtype=torch.int32, device="cuda")  # any element type
     assert int(c.cider_moe_plan(ids, 9, workspace=wide)[0][1]) == 12000
+
+
+def test_sizes_past_32_bits_are_refused():
+    c = cider()
+    with pytest.raises(ValueError):
+        c.cider_moe_plan(torch.zeros(4, 1, dtype=torch.int32, device="cuda"), (1 << 32) + 8)
+    x, sx, w, sw, off, idx = (v.cuda() for v in make([3, 4], 32, 64, 8, seed=11, T=5))
+    for div in (1 << 31, (1 << 32) + 1, 1 - (1 << 32), -1):
+        with pytest.raises((ValueError, c.CiderError)):
+            c.cider_w8a8_grouped_gemm(x, sx, w, sw, off, row_index=idx, row_div=div)
+    y = c.cider_w8a8_grouped_gemm(x, sx, w, sw, off, row_index=idx, row_div=(1 << 31) - 1)   # all of them row 0
+    o = c.cider_w8a8_grouped_gemm(x, sx, w, sw, off, row_index=torch.zeros_like(idx))
+    assert torch.equal(y, o)

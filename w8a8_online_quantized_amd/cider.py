@@ -566,8 +566,13 @@ def _raw_stream(stream, dev):
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
+_I32 = 1 << 31
+
+
 def cider_moe_plan_workspace_size(T: int, top_k: int, n_experts: int) -> int:
     """Workspace bytes cider_moe_plan needs (0: one launch, no workspace)."""
+    if not (-_I32 <= top_k < _I32 and -_I32 <= n_experts < _I32):
+        raise ValueError("invalid routing sizes")   # (ctypes would take them modulo 2^32)
     n = lib().cider_moe_plan_workspace_size(T, top_k, n_experts)
     if n < 0:
         raise ValueError("invalid routing sizes")
@@ -626,6 +631,8 @@ def _grouped(fn, gated, bits, x_q, x_scale, w, w_scale, offsets, row_index, row_
     if row_index is not None:
         P, index = row_index.numel(), row_index.data_ptr()
         _need_on(dev, row_index, torch.int32, (P,), "row_index")
+    if not -_I32 <= row_div < _I32:
+        raise ValueError("row_div must be from 1 to 2^31 - 1")   # (ctypes would take it modulo 2^32)
     if gated and N % 2:
         raise ValueError("the gated product needs as many gate rows as up rows")
     n_out = N // 2 if gated else N
