@@ -791,7 +791,8 @@ def w8a8_moe(x_q, x_scale, expert_ids, gate_up, gate_up_scale, down, down_scale,
     """The experts of a block on the tokens' codes (from cider_norm_quant or
     cider_quant_act): gate_up int8 [E, 2I, K] or packed uint8 [E, 2I, K/2],
     down [E, N, I] likewise. Returns (expert rows [T * top_k, N], slots), which
-    cider_norm_quant sums into the residual."""
+    cider_norm_quant sums into the residual. Ids of no expert have slot -1, and
+    as many of the last expert rows hold nothing that was written."""
     import torch
     t = out_dtype or torch.float16
     top_k, E = expert_ids.shape[1], gate_up.shape[0]

@@ -515,6 +515,9 @@ grouped_kernel(const GroupedArgs g) {
     }
     return;
   }
+  // Rows that are not whole 16-byte chunks: single elements straight from the
+  // fragments. Few rows do not feel it (308 int4 rows of 1003 or 1008 columns 9.0
+  // us); 32768 rows of 2047 columns with K = 1024 take 180 us, of 2048 95.
 #pragma unroll
   for (int b = 0; b < TM; ++b) {
     const int m = wm + 16 * b + l16;

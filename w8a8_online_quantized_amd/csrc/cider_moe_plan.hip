@@ -15,9 +15,10 @@
 // Latency-bound at decode sizes, so one workgroup does everything in one
 // launch up to kOneBlockIds ids; beyond, a first launch counts each block's
 // ids and a second one places them, every block summing the counts of the
-// blocks before it by itself. Kernel times (HIP events): 128 ids 3.5 us (an
-// empty launch), 4096 ids 6.0, 8192 ids 8.4 (7.7 in two launches), 262144 ids
-// 11.6 (3.1 MB; the scattered 4-byte stores and the two launches bound it).
+// blocks before it by itself. Kernel times (HIP events): 128 ids 3.4-3.9 us (an
+// empty launch 3.5), 4096 ids 5.9, 8192 ids 8.5, 262144 ids 11.5 (3.1 MB; two
+// launches, the second of which counts its ids again, and scattered 4-byte
+// stores bound it).
 #include "cider_internal.h"
 
 namespace cider {
@@ -25,6 +26,10 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / 64;
+// One launch or two. The kernels alone cross near 6500 ids (64 experts, one /
+// two: 4096 ids 5.9 / 7.7 us, 6144 7.2 / 7.7, 8192 8.5 / 7.8; 512 experts, 8192
+// ids: 10.1 / 10.5), but two launches also need a workspace: 8192 ids from
+// Python take 8.9 / 13.2 us among others and 24.4 / 25.9 alone.
 constexpr int kOneBlockIds = 8192;
 constexpr int kMaxBlocks = 256;
 
@@ -211,7 +216,7 @@ hipError_t launch_moe_plan(const int32_t* ids, int64_t P, int E, int32_t* offset
   const PlanShape s = plan_shape(P, E);
   int bits = 1;
   while ((1 << bits) < E) ++bits;
-  const size_t lds = (size_t)(kWaves * E + kWaves + 2 * kThreads) * 4;   // at most 40 KB
+  const size_t lds = (size_t)(kWaves * E + kWaves + 2 * kThreads) * 4;   // at most 41 KB
   int32_t* counts = s.blocks > 1 ? static_cast<int32_t*>(ws) : nullptr;
   if (counts) {
     plan_count<<<dim3((unsigned)s.blocks), dim3(kThreads), lds, stream>>>(ids, P, s.chunk, E, counts);

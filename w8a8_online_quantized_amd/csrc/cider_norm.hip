@@ -23,11 +23,13 @@
 // HBM-bound: each of x and the block's rows is read once, h and the codes are
 // written once. The row stays in registers from the first load to the codes.
 // Kernel times (HIP events): 4096 rows of 2560 fp16 with both norms and a gate
-// 16.5 us (73 MB, 4.5 TB/s), 4096 rows of 2048 bf16 each summing 8 expert rows
-// 31.2 us (177 MB, 5.7 TB/s; a plain copy reaches 5.1), one row 4.1 us (an empty
-// launch takes 3.5). Loads as address-space-1 vectors took these from 29.4
-// and 38.9 us to 17.8 and 37.1: the compiler had made flat one-dword loads of
-// them; past-the-cache loads and stores did the rest (load16_once).
+// 16.6 us (73 MB, 4.4 TB/s), 4096 rows of 2048 bf16 each summing 8 expert rows
+// 31.1 us (177 MB, 5.7 TB/s; six in seven of them reads, which a plain read
+// stream takes at 6.2 and a copy at 5.1), one row 4.1 us (an empty launch takes
+// 3.5). Rows that take norm_rows_loop are far from this (see there). Loads as
+// address-space-1 vectors took these from 29.4 and 38.9 us to 17.8 and 37.1: the
+// compiler had made flat one-dword loads of them; past-the-cache loads and stores
+// did the rest (load16_once).
 #include "cider_internal.h"
 #include "cider_quant_rule.h"
 
@@ -322,7 +324,11 @@ __global__ void __launch_bounds__(kThreads) norm_rows_reg(const NormArgs a) {
 // 8 != 0 (VEC = 1, one element at a time; per-row scale). One workgroup per
 // row, three passes over it: sum of p^2 (with a post-norm), then h, its sum of
 // squares and max|h * w|, then the codes from h read back (each thread reads
-// only what it wrote itself). The block's rows are read twice with a post-norm.
+// only what it wrote itself). The block's rows are read twice with a post-norm,
+// and slots and weights again for every chunk. With both norms and a gate, 4096
+// rows of 12288 fp16 take 105 us (352 MB, at the copy rate 69) and of 2047 43
+// (11); summing 8 expert rows, 2048 rows of 12288 bf16 192 us (528 MB, at the read
+// rate 85) and 4096 rows of 2047 169 (28).
 template <int VEC, bool BF>
 __global__ void __launch_bounds__(kThreads) norm_rows_loop(const NormArgs a) {
   __shared__ float red[2][2 * kWaves];
@@ -459,9 +465,11 @@ hipError_t launch_norm_t(const NormArgs& a, hipStream_t st) {
   // of 2 chunks 6.4 us, four of 1 4.8; K = 2560 two of 3 8.8, four of 2 6.8;
   // one row 6.1 / 5.2), except up to K = 512, which one wave of 1 holds. With more
   // rows idle lanes cost: one wave up to K = 1024 (2048 rows 4.9 us, four waves
-  // 5.3), four at K = 2048 (4096 rows summing 8: 31.2 us, two waves 33.0, one 36.6),
+  // 5.3), four from there to K = 2048 (4096 rows of 2048 summing 8: 31.1 us, two
+  // waves 33.0, one 36.6; of 1536 24.7, two 26.9, one of 3 chunks 24.5; at K = 1280
+  // one of 3 is the faster, 21.3 to 22.0, and without expert rows 10.1 to 12.1),
   // two where four would leave most of their second chunks idle (4096 rows of
-  // 2560 with both norms and a gate: 16.5 us, four waves 18.9, one 16.7).
+  // 2560 with both norms and a gate: 16.6 us, four waves 18.9, one 16.7).
   const dim3 block(kThreads);
   const unsigned rows1 = (unsigned)a.M, rows2 = (rows1 + 1) / 2, rows4 = (rows1 + 3) / 4;
   const int64_t C = a.K / 8;                     // 16-byte chunks per row
@@ -488,7 +496,8 @@ __device__ __forceinline__ float code_value(int8_t q, float s) {
 }
 
 // y = fp(code * scale), 8 codes per thread when rows are whole 8-byte chunks
-// (scale groups are multiples of 8), else one.
+// (scale groups are multiples of 8), else one (4096 rows of 2048 4.6 us, of 2047
+// 13.5).
 template <int VEC, bool BF>
 __global__ void __launch_bounds__(kThreads) dequant_rows(const int8_t* __restrict__ q, const float* __restrict__ s,
                                                          int64_t M, int K, int group_size, uint16_t* __restrict__ y) {
