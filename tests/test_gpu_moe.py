@@ -670,3 +670,52 @@ def test_sizes_past_32_bits_are_refused():
     y = c.cider_w8a8_grouped_gemm(x, sx, w, sw, off, row_index=idx, row_div=(1 << 31) - 1)   # all of them row 0
     o = c.cider_w8a8_grouped_gemm(x, sx, w, sw, off, row_index=torch.zeros_like(idx))
     assert torch.equal(y, o)
+
+
+def test_captured_blocks_that_make_their_own_workspace():
+    """Two captured blocks of more ids than one launch takes, replayed by turns between eager calls."""
+    c = cider()
+    E, I, H, k, T = 6, 64, 128, 3, 3100
+    gu, dn = moe_weights(E, I, H, 25)
+    nw = torch.ones(H, dtype=torch.bfloat16, device="cuda")
+    assert c.cider_moe_plan_workspace_size(T, k, E) > 0
+    both = []
+    for _ in range(2):
+        x = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+        ids, w = torch.zeros(T, k, dtype=torch.int32, device="cuda"), torch.zeros(T, k, device="cuda")
+        block(c, x, ids, w, nw, gu, dn)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = block(c, x, ids, w, nw, gu, dn)
+        both.append((x, ids, w, graph, out))
+    for seed in range(3):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        for x, ids, w, graph, _ in both:
+            x.copy_(torch.randn(T, H, generator=g, device="cuda"))
+            ids.copy_(torch.randint(-1, E + 1, (T, k), generator=g, device="cuda"))
+            w.copy_(torch.rand(T, k, generator=g, device="cuda"))
+            graph.replay()
+        eager = [block(c, x, ids, w, nw, gu, dn) for x, ids, w, _, _ in both]
+        torch.cuda.synchronize()
+        for (_, _, _, _, out), o in zip(both, eager):
+            for a, b in zip(out, o):
+                assert torch.equal(a, b), seed
+
+
+def test_nan_in_what_nothing_reads():
+    """Rows, scales and experts that no group names, and the weights of dropped slots, may hold NaN."""
+    c = cider()
+    x, sx, w, sw, off, idx = (v.cuda() for v in make([5, 0, 9], 48, 64, 8, seed=13, T=20, k=1))
+    idx = idx.remainder(10)                                          # rows 10 .. 19 are read by no one
+    y = c.cider_w8a8_grouped_gemm(x, sx, w, sw, off, row_index=idx)
+    sx2, sw2 = sx.clone(), sw.clone()
+    sx2[10:], sw2[1] = float("nan"), float("nan")
+    rows = torch.cat((c.cider_w8a8_grouped_gemm(x, sx2, w, sw2, off, row_index=idx), torch.full_like(y[:4], float("nan"))))
+    assert torch.equal(rows[:14], y)
+    slots = torch.tensor([[0, -1, 13], [-5, 18, 99], [7, 7, -1]], dtype=torch.int32, device="cuda")
+    wt = torch.rand(3, 3, device="cuda")
+    there = (slots >= 0) & (slots < 18)
+    a = c.cider_norm_quant(None, rows, slots=slots, weights=torch.where(there, wt, float("nan")))[0]
+    b = c.cider_norm_quant(None, rows, slots=slots, weights=torch.where(there, wt, 0.0))[0]
+    assert torch.equal(a, b) and bool(a.isfinite().all()) and not bool(a[1].any())
