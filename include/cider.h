@@ -542,6 +542,188 @@ cider_status_t cider_norm_quant(const cider_norm_quant_t* args, void* stream);
 cider_status_t cider_dequant_act(const int8_t* x_q, const float* x_scale, int64_t M, int64_t K,
                                  int32_t group_size, void* y, int32_t y_dtype, void* stream);
 
+/* ---- Attention blocks ---------------------------------------------------------
+ * What stands between the q/k/v projections and the output projection of a
+ * decoder layer: rotary positions, a paged cache of keys and values in 4 bits,
+ * and attention over it. In the order of use, for T tokens:
+ *   cider_w8a8_gemm_split_dt      codes -> q, k, v rows
+ *   cider_kv4_append              head norms, rotation; k and v into the cache
+ *   cider_kv4_attention           q over the cache's pages -> rows
+ *   cider_quant_act_dt            those rows -> codes of the output projection
+ * Lengths, pages and slots are read on the device, and no size is returned to
+ * the host, so the chain can be captured into a HIP graph and replayed for
+ * other lengths, pages and slots.
+ */
+
+#define CIDER_ROPE_MAX_HEAD_DIM 1024
+#define CIDER_ROPE_MAX_ROTARY_DIM 512
+#define CIDER_ROPE_MAX_HEADS 65536
+#define CIDER_KV4_MAX_PAGE_SIZE 1024
+#define CIDER_KV4_MAX_HEADS 1024
+#define CIDER_KV4_MAX_Q_HEADS 16384
+
+/* Rotary positions. The first rotary_dim dimensions of each head are pairs
+ * (half layout: i and i + rotary_dim/2; interleaved: 2i and 2i + 1), and pair i
+ * of a token at position p turns by the angle p * inv_freq[i]:
+ *   u' = scale * (u cos - w sin),  w' = scale * (w cos + u sin),
+ * the angle reduced in fp64, the rest in fp32, rounded once. Dimensions behind
+ * rotary_dim are copied. Frequencies scaled for long contexts, and the factor
+ * that goes with them, are the caller's inv_freq and scale.
+ *   x, y      : fp16 or bf16 (dtype) [T, heads, head_dim] with the given strides
+ *               (in elements; a head's dimensions are contiguous). y may be x
+ *               with the same strides, and must not overlap it otherwise.
+ *   positions : int32 [T], any sign.
+ *   inv_freq  : fp64 [rotary_dim / 2].
+ * T < 2^23; heads <= CIDER_ROPE_MAX_HEADS; 2 <= head_dim <=
+ * CIDER_ROPE_MAX_HEAD_DIM; rotary_dim even, at most head_dim and
+ * CIDER_ROPE_MAX_ROTARY_DIM. Head sizes and strides that are not multiples of
+ * 8, and half layouts whose rotary_dim is not one of 16, take a slower path
+ * with the same results. (T, heads, head_dim) whose grid would take 2^31 GPU
+ * threads return CIDER_ERROR_INVALID_VALUE. */
+typedef struct {
+  const void* x;
+  const int32_t* positions;
+  const double* inv_freq;
+  void* y;
+  int64_t T;
+  int64_t x_row_stride, x_head_stride, y_row_stride, y_head_stride;
+  int32_t dtype; /* a cider_dtype_t */
+  int32_t heads;
+  int32_t head_dim;
+  int32_t rotary_dim;
+  int32_t interleaved; /* 0 or 1 */
+  float scale;
+} cider_rope_t;
+cider_status_t cider_rope(const cider_rope_t* args, void* stream);
+
+/* A paged cache of keys and values in 4 bits, in four arrays of the caller's:
+ *   k_codes, v_codes : uint8 [n_pages, kv_heads, page_size, head_dim / 2], the
+ *       code c in -7 .. 7 as the nibble c + 8, low nibble first. k_codes holds
+ *       a head's dimensions in order. v_codes holds them as [16][G][head_dim /
+ *       16 / G], G = head_dim / group_size: dimension g * group_size + u *
+ *       (head_dim / 16 / G) + r is code (u * G + g) * (head_dim / 16 / G) + r
+ *       (in order for G = 1).
+ *   k_scale, v_scale : fp32 [n_pages, kv_heads, G, page_size].
+ * A token's place is its slot, page * page_size + offset. head_dim 64, 128 or
+ * 256; group_size 0 (a whole head) or head_dim, head_dim / 2 or head_dim / 4,
+ * at least 32; page_size a power of two from 16 to CIDER_KV4_MAX_PAGE_SIZE;
+ * kv_heads <= CIDER_KV4_MAX_HEADS; n_pages * page_size < 2^31. Pages are
+ * copied, moved and shared by copying the arrays' first dimension and editing
+ * page tables. */
+typedef struct {
+  uint8_t* k_codes;
+  float* k_scale;
+  uint8_t* v_codes;
+  float* v_scale;
+  int64_t n_pages;
+  int32_t page_size;
+  int32_t kv_heads;
+  int32_t head_dim;
+  int32_t group_size;
+} cider_kv4_cache_t;
+
+/* New tokens into the cache, in one launch with what q and k go through before.
+ * Per token t and head, in fp32:
+ *   n     = x / sqrt(mean(x^2) + eps) * norm    (q with q_norm, k with k_norm)
+ *   n     = n rotated as by cider_rope          (q and k, with positions)
+ *   q_out = fp(n);  k = fp(n), v as given, and both by the int4 rule of
+ *           cider_quant_weight per head and group of dimensions
+ *           (s = max|.| / 7, code = clamp(round_half_even(. / s))) into slot
+ *           slots[t]; nothing else of the cache changes.
+ * A token whose slot is outside [0, n_pages * page_size) (a padded one) is not
+ * stored; its q is still written. The slots of a call must differ: tokens that
+ * share one leave codes and scales of either in it. A group of k or v that
+ * holds an infinity or a NaN is stored with the scale NaN and codes 0, so the
+ * rows that attend to it become NaN and no others.
+ *   q, q_out [T, q_heads, head_dim] (both or neither; q_out may be q), k, v [T,
+ *   kv_heads, head_dim], fp16 or bf16 (dtype), strides in elements, multiples
+ *   of 8; q_norm, k_norm [head_dim] or NULL; positions int32 [T] and inv_freq
+ *   fp64 [rotary_dim / 2] (both or neither); slots int32 [T].
+ * T < 2^23, q_heads <= CIDER_KV4_MAX_Q_HEADS, rotary_dim a multiple of 16 up
+ * to head_dim, eps positive and finite with a norm. */
+typedef struct {
+  cider_kv4_cache_t cache;
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* q_norm;
+  const void* k_norm;
+  const int32_t* positions;
+  const double* inv_freq;
+  const int32_t* slots;
+  void* q_out;
+  int64_t T;
+  int64_t q_row_stride, q_head_stride, k_row_stride, k_head_stride, v_row_stride, v_head_stride;
+  int64_t out_row_stride, out_head_stride; /* of q_out */
+  int32_t dtype; /* a cider_dtype_t */
+  int32_t q_heads;
+  int32_t rotary_dim;
+  int32_t interleaved; /* 0 or 1 */
+  float rope_scale;
+  float eps;
+} cider_kv4_append_t;
+cider_status_t cider_kv4_append(const cider_kv4_append_t* args, void* stream);
+
+/* The cache's rows at slots [n], for consumers that are not quantized:
+ *   k, v [n, kv_heads, head_dim] = fp((float)code * scale), fp16 or bf16
+ *   (dtype), contiguous; zeros for a slot outside [0, n_pages * page_size).
+ * The same slot may come several times. n < 2^31. */
+cider_status_t cider_kv4_read(const cider_kv4_cache_t* cache, const int32_t* slots, int64_t n, void* k, void* v,
+                              int32_t dtype, void* stream);
+
+/* Attention over the cache's pages:
+ *   y[t,h] = sum_j softmax_j(softmax_scale * q[t,h] . k_j) v_j
+ * over the tokens j of t's sequence that it sees, with key/value head
+ * h / (q_heads / kv_heads).
+ *   q          : [T, q_heads, head_dim] fp16 or bf16 (dtype), strides in
+ *                elements, multiples of 8.
+ *   lengths    : int32 [B] on the device: tokens of each sequence in the cache,
+ *                those of its queries included. Clamped to 0 .. max_pages *
+ *                page_size.
+ *   page_table : int32 [B, max_pages] on the device: the pages of a sequence in
+ *                order. Entries that no visible token needs are not used; the
+ *                tokens of a page outside [0, n_pages) are not seen.
+ *   query_offsets : int32 [B + 1] on the device: sequence b has the query rows
+ *                query_offsets[b] .. query_offsets[b+1] - 1, ascending from 0 to
+ *                at most T (offsets that do not ascend are clamped to it, and
+ *                rows that come in two sequences are then written by either);
+ *                or NULL: T / B rows each, T a multiple of B. Rows of no
+ *                sequence are left as they were.
+ *   y          : [T, q_heads, head_dim], contiguous; must not overlap q.
+ *   causal     : 1: query i of n is at position p = length - n + i and sees the
+ *                tokens j <= p. 0: it sees all tokens of its sequence.
+ *   window     : 0, or the tokens j > p - window only.
+ * A row that sees no token is zeros. Scores and the softmax's sums are fp32;
+ * the weights are rounded to fp16 (11 bits) once they are multiplied by V's
+ * scale. exp2 is the GPU's fp32 instruction.
+ * workspace: 16-byte aligned, at least cider_kv4_attention_workspace_size bytes
+ * (capacity = max_pages * page_size; 0: none, NULL then). Its contents are
+ * scratch; calls that share one must not overlap in time. The result depends
+ * on T, B and the capacity through the order of its sums, and on nothing else
+ * but the inputs. T * q_heads < 2^31, B >= 1, capacity < 2^31, softmax_scale finite;
+ * sizes whose grid would take 2^31 GPU threads return
+ * CIDER_ERROR_INVALID_VALUE. */
+typedef struct {
+  cider_kv4_cache_t cache;
+  const void* q;
+  const int32_t* page_table;
+  const int32_t* lengths;
+  const int32_t* query_offsets;
+  void* y;
+  void* workspace;
+  int64_t workspace_bytes;
+  int64_t T, B, max_pages;
+  int64_t q_row_stride, q_head_stride;
+  int32_t dtype; /* a cider_dtype_t */
+  int32_t q_heads;
+  int32_t causal; /* 0 or 1 */
+  int32_t window;
+  float softmax_scale;
+} cider_kv4_attention_t;
+int64_t cider_kv4_attention_workspace_size(int64_t T, int64_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                           int64_t capacity);
+cider_status_t cider_kv4_attention(const cider_kv4_attention_t* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

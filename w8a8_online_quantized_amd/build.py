@@ -14,7 +14,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libcider.so")
 SOURCES = ["cider_api.hip", "cider_quant.hip", "cider_gemm.hip", "cider_mv.hip", "cider_probe.hip",
-           "cider_grouped.hip", "cider_moe_plan.hip", "cider_norm.hip"]
+           "cider_grouped.hip", "cider_moe_plan.hip", "cider_norm.hip", "cider_rope.hip", "cider_kv4_cache.hip",
+           "cider_kv4_attention.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",

@@ -11,8 +11,10 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import functools
+import math
 import os
 import re
+import typing
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG_DIR, "libcider.so")
@@ -78,6 +80,11 @@ SIGNATURES = {
                     "cider_w4a8_grouped_swiglu")},
     "cider_norm_quant": (ctypes.c_int, [_c_p, _c_p]),
     "cider_dequant_act": (ctypes.c_int, [_c_p, _c_p, _c_i64, _c_i64, _c_i32, _c_p, _c_i32, _c_p]),
+    "cider_rope": (ctypes.c_int, [_c_p, _c_p]),
+    "cider_kv4_append": (ctypes.c_int, [_c_p, _c_p]),
+    "cider_kv4_read": (ctypes.c_int, [_c_p, _c_p, _c_i64, _c_p, _c_p, _c_i32, _c_p]),
+    "cider_kv4_attention_workspace_size": (ctypes.c_int64, [_c_i64, _c_i64, _c_i32, _c_i32, _c_i32, _c_i64]),
+    "cider_kv4_attention": (ctypes.c_int, [_c_p, _c_p]),
 }
 
 STACK_PROJECTIONS = ("q", "k", "v", "o", "gate", "up", "down")
@@ -97,6 +104,42 @@ class NormQuant(ctypes.Structure):
                [(n, ctypes.c_int64) for n in ("M", "K", "block_rows", "rows_per_gate")] + \
                [(n, ctypes.c_int32) for n in ("dtype", "top_k", "group_size")] + \
                [("alpha", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+class Rope(ctypes.Structure):
+    """cider_rope_t."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("x", "positions", "inv_freq", "y")] + \
+               [(n, ctypes.c_int64) for n in ("T", "x_row_stride", "x_head_stride", "y_row_stride", "y_head_stride")] + \
+               [(n, ctypes.c_int32) for n in ("dtype", "heads", "head_dim", "rotary_dim", "interleaved")] + \
+               [("scale", ctypes.c_float)]
+
+
+class Kv4CacheArrays(ctypes.Structure):
+    """cider_kv4_cache_t: the cache's device pointers and sizes."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_codes", "k_scale", "v_codes", "v_scale")] + \
+               [("n_pages", ctypes.c_int64)] + \
+               [(n, ctypes.c_int32) for n in ("page_size", "kv_heads", "head_dim", "group_size")]
+
+
+class Kv4Append(ctypes.Structure):
+    """cider_kv4_append_t (None leaves a part out)."""
+    _fields_ = [("cache", Kv4CacheArrays)] + \
+               [(n, ctypes.c_void_p) for n in ("q", "k", "v", "q_norm", "k_norm", "positions", "inv_freq", "slots",
+                                               "q_out")] + \
+               [(n, ctypes.c_int64) for n in ("T", "q_row_stride", "q_head_stride", "k_row_stride", "k_head_stride",
+                                              "v_row_stride", "v_head_stride", "out_row_stride", "out_head_stride")] + \
+               [(n, ctypes.c_int32) for n in ("dtype", "q_heads", "rotary_dim", "interleaved")] + \
+               [("rope_scale", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+class Kv4Attention(ctypes.Structure):
+    """cider_kv4_attention_t."""
+    _fields_ = [("cache", Kv4CacheArrays)] + \
+               [(n, ctypes.c_void_p) for n in ("q", "page_table", "lengths", "query_offsets", "y", "workspace")] + \
+               [(n, ctypes.c_int64) for n in ("workspace_bytes", "T", "B", "max_pages", "q_row_stride",
+                                              "q_head_stride")] + \
+               [(n, ctypes.c_int32) for n in ("dtype", "q_heads", "causal", "window")] + \
+               [("softmax_scale", ctypes.c_float)]
 
 
 _lib = None
@@ -803,6 +846,293 @@ def w8a8_moe(x_q, x_scale, expert_ids, gate_up, gate_up_scale, down, down_scale,
                 stream=stream)
     a_q, a_scale = cider_quant_act(a, 0, stream=stream)
     return down_call(a_q, a_scale, down, down_scale, offsets, out_dtype=t, stream=stream), slots
+
+
+# ---- attention blocks -------------------------------------------------------
+
+class KV4Cache(typing.NamedTuple):
+    """A paged cache of keys and values in 4 bits (cider_kv4_cache_t in
+    include/cider.h): k_codes, v_codes uint8 [n_pages, kv_heads, page_size,
+    head_dim / 2], k_scale, v_scale fp32 [n_pages, kv_heads, G, page_size]."""
+    k_codes: typing.Any
+    k_scale: typing.Any
+    v_codes: typing.Any
+    v_scale: typing.Any
+
+
+def kv4_cache(n_pages: int, kv_heads: int, page_size: int, head_dim: int, group_size: int = 0, device=None) -> KV4Cache:
+    """An empty KV4Cache (codes 0, scales 0) on the current device. group_size 0
+    gives one scale per token and head, 32 or more one per group of dimensions."""
+    import torch
+    G = head_dim // group_size if group_size else 1
+    device = device or torch.device("cuda", torch.cuda.current_device())
+    codes, scale = (n_pages, kv_heads, page_size, head_dim // 2), (n_pages, kv_heads, G, page_size)
+    return KV4Cache(torch.full(codes, 0x88, dtype=torch.uint8, device=device), torch.zeros(scale, device=device),
+                    torch.full(codes, 0x88, dtype=torch.uint8, device=device), torch.zeros(scale, device=device))
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+                     trained: int = 8192, fast: float = 32.0, slow: float = 1.0, device=None):
+    """(inv_freq fp64 [rotary_dim / 2] on the GPU, scale) for cider_rope and
+    cider_kv4_append: base^(-2i/rotary_dim), scaled for contexts `factor` times
+    the `trained` length:
+
+    * None: as they are;
+    * "linear": divided by factor (positions interpolated);
+    * "base": base times factor^(d / (d - 2)), so that the slowest pair turns
+      factor times slower and the fastest as before;
+    * "parts": pairs that turn less than `slow` times over the trained length
+      divided by factor, those that turn more than `fast` times as they are, a
+      ramp between, and scale 0.1 ln(factor) + 1 (Peng et al., YaRN, 2023)."""
+    import torch
+    if rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be even and at least 2")
+    if not factor >= 1.0 or not base > 1.0 or not math.isfinite(base * factor):
+        raise ValueError("factor must be at least 1 and base above 1")
+    d, scale = rotary_dim, 1.0
+    if scaling == "base":
+        base = base * factor ** (d / (d - 2)) if d > 2 else base
+    freq = [base ** (-2.0 * i / d) for i in range(d // 2)]
+    if scaling == "linear":
+        freq = [f / factor for f in freq]
+    elif scaling == "parts":
+        if trained < 1 or not fast > slow > 0:
+            raise ValueError("parts need a trained length and fast > slow > 0")
+        pair = lambda turns: d * math.log(trained / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))  # noqa: E731
+        lo, hi = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), d - 1)
+        ramp = [min(max((i - lo) / max(hi - lo, 1e-3), 0.0), 1.0) for i in range(d // 2)]
+        freq = [f / factor * r + f * (1.0 - r) for f, r in zip(freq, ramp)]
+        scale = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "base"):
+        raise ValueError("scaling must be None, 'linear', 'base' or 'parts'")
+    device = device or torch.device("cuda", torch.cuda.current_device())
+    return torch.tensor(freq, dtype=torch.float64, device=device), scale
+
+
+def _need_rows(dev, t, dtype, shape, name):
+    """A [T, heads, D] tensor on the current device whose heads are contiguous:
+    its (row, head) strides. A dimension of one has a stride of its own."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the current device {dev}, not {t.get_device()}")
+    T, H, D = shape
+    row, head, one = t.stride()
+    if one != 1 and D > 1:
+        raise ValueError(f"{name} must have contiguous heads")
+    head = head if H > 1 else D
+    return (row if T > 1 else H * D), head
+
+
+def _cache_args(dev, cache):
+    import torch
+    k_codes = cache.k_codes
+    n_pages, hkv, page, half = k_codes.shape
+    G = cache.k_scale.shape[2]
+    codes, scales = (n_pages, hkv, page, half), (n_pages, hkv, G, page)
+    _need_on(dev, k_codes, torch.uint8, codes, "k_codes")
+    _need_on(dev, cache.v_codes, torch.uint8, codes, "v_codes")
+    _need_on(dev, cache.k_scale, torch.float32, scales, "k_scale")
+    _need_on(dev, cache.v_scale, torch.float32, scales, "v_scale")
+    D = 2 * half
+    if not G or D % G or max(page, hkv, D) >= _I32:
+        raise ValueError("the cache's groups must divide its heads")
+    return Kv4CacheArrays(k_codes.data_ptr(), cache.k_scale.data_ptr(), cache.v_codes.data_ptr(), cache.v_scale.data_ptr(),
+                          n_pages, page, hkv, D, D // G)
+
+
+def _rotation(dev, T, positions, inv_freq):
+    import torch
+    _need_on(dev, positions, torch.int32, (T,), "positions")
+    _need_on(dev, inv_freq, torch.float64, (inv_freq.numel(),), "inv_freq")
+    if 2 * inv_freq.numel() >= _I32:
+        raise ValueError("too many frequencies")
+    return positions.data_ptr(), inv_freq.data_ptr(), 2 * inv_freq.numel()
+
+
+@_on_stream
+def cider_rope(x, positions, inv_freq, interleaved: bool = False, scale: float = 1.0, y=None, stream=None):
+    """Rotary positions: x [T, heads, D] (fp16 or bf16, heads contiguous) with
+    the first 2 * len(inv_freq) dimensions of each head turned by positions
+    (int32 [T]) times inv_freq (fp64) -> y, x's shape, contiguous unless given
+    (y may be x). See cider_rope in include/cider.h; rope_frequencies makes
+    inv_freq and scale."""
+    import torch
+    dev = torch.cuda.current_device()
+    T, H, D = shape = tuple(x.shape)
+    xr, xh = _need_rows(dev, x, x.dtype, shape, "x")
+    pos, freq, rd = _rotation(dev, T, positions, inv_freq)
+    if y is None:
+        y = torch.empty(shape, dtype=x.dtype, device=x.device)
+    yr, yh = _need_rows(dev, y, x.dtype, shape, "y")
+    args = Rope(x.data_ptr(), pos, freq, y.data_ptr(), T, xr, xh, yr, yh, _fp_code(x, "x"), min(H, _I32 - 1),
+                min(D, _I32 - 1), rd, 1 if interleaved else 0, scale)
+    st = lib().cider_rope(ctypes.byref(args), _raw_stream(stream, dev))
+    if st:
+        _check("cider_rope", st)
+    return y
+
+
+@_on_stream
+def cider_kv4_append(cache, k, v, slots, q=None, positions=None, inv_freq=None, interleaved: bool = False,
+                     rope_scale: float = 1.0, q_norm=None, k_norm=None, eps: float = 1e-6, q_out=None, stream=None):
+    """New tokens' k, v [T, kv_heads, D] into a KV4Cache at slots (int32 [T],
+    page * page_size + offset; outside the cache: not stored), after k's head
+    norm (k_norm [D]) and rotation (positions, inv_freq), where given. q [T,
+    q_heads, D] goes through q_norm and the rotation to q_out, which is
+    returned (contiguous unless given; it may be q). See cider_kv4_append in
+    include/cider.h. The slots of a call must differ."""
+    import torch
+    dev = torch.cuda.current_device()
+    arrays = _cache_args(dev, cache)
+    T, t, D, Hkv = k.shape[0], k.dtype, arrays.head_dim, arrays.kv_heads
+    kr, kh = _need_rows(dev, k, t, (T, Hkv, D), "k")
+    vr, vh = _need_rows(dev, v, t, (T, Hkv, D), "v")
+    _need_on(dev, slots, torch.int32, (T,), "slots")
+    pq = pqn = pkn = pos = freq = po = None
+    qr = qh = our = ouh = Hq = rd = 0
+    if q is not None:
+        Hq = q.shape[1]
+        if Hq >= _I32:
+            raise ValueError("too many query heads")
+        qr, qh = _need_rows(dev, q, t, (T, Hq, D), "q")
+        if q_out is None:
+            q_out = torch.empty(T, Hq, D, dtype=t, device=q.device)
+        our, ouh = _need_rows(dev, q_out, t, (T, Hq, D), "q_out")
+        pq, po = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None or q_norm is not None:
+        raise ValueError("q_out and q_norm need q")
+    if q_norm is not None:
+        _need_on(dev, q_norm, t, (D,), "q_norm")
+        pqn = q_norm.data_ptr()
+    if k_norm is not None:
+        _need_on(dev, k_norm, t, (D,), "k_norm")
+        pkn = k_norm.data_ptr()
+    if positions is not None:
+        if inv_freq is None:
+            raise ValueError("positions need inv_freq")
+        pos, freq, rd = _rotation(dev, T, positions, inv_freq)
+    elif inv_freq is not None:
+        raise ValueError("inv_freq needs positions")
+    args = Kv4Append(arrays, pq, k.data_ptr(), v.data_ptr(), pqn, pkn, pos, freq, slots.data_ptr(), po, T, qr, qh, kr, kh,
+                     vr, vh, our, ouh, _fp_code(k, "k"), Hq, rd, 1 if interleaved else 0, rope_scale, eps)
+    st = lib().cider_kv4_append(ctypes.byref(args), _raw_stream(stream, dev))
+    if st:
+        _check("cider_kv4_append", st)
+    return q_out
+
+
+@_on_stream
+def cider_kv4_read(cache, slots, k=None, v=None, stream=None, out_dtype=None):
+    """The cache's rows at slots (int32 [n]) -> (k, v) [n, kv_heads, D], fp16 or
+    (out_dtype or a given k) bf16; zeros for slots outside the cache."""
+    import torch
+    dev = torch.cuda.current_device()
+    arrays = _cache_args(dev, cache)
+    n = slots.numel()
+    shape = (n, arrays.kv_heads, arrays.head_dim)
+    _need_on(dev, slots, torch.int32, (n,), "slots")
+    if k is None:
+        k = torch.empty(shape, dtype=out_dtype or (v.dtype if v is not None else torch.float16), device=slots.device)
+    else:
+        _need_on(dev, k, k.dtype, shape, "k")
+    if v is None:
+        v = torch.empty_like(k)
+    else:
+        _need_on(dev, v, k.dtype, shape, "v")
+    st = lib().cider_kv4_read(ctypes.byref(arrays), slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), _fp_code(k, "k"),
+                              _raw_stream(stream, dev))
+    if st:
+        _check("cider_kv4_read", st)
+    return k, v
+
+
+def cider_kv4_attention_workspace_size(T: int, B: int, q_heads: int, kv_heads: int, head_dim: int, capacity: int) -> int:
+    """Workspace bytes cider_kv4_attention needs for T query rows of B sequences
+    whose page tables hold `capacity` tokens (0: one launch, no workspace)."""
+    if not all(-_I32 <= n < _I32 for n in (q_heads, kv_heads, head_dim)):
+        raise ValueError("invalid attention sizes")   # (ctypes would take them modulo 2^32)
+    n = lib().cider_kv4_attention_workspace_size(T, B, q_heads, kv_heads, head_dim, capacity)
+    if n < 0:
+        raise ValueError("invalid attention sizes")
+    return n
+
+
+_attention_workspace_size = functools.lru_cache(maxsize=256)(cider_kv4_attention_workspace_size)
+
+
+@_on_stream
+def cider_kv4_attention(q, cache, page_table, lengths, query_offsets=None, causal: bool = True, window: int = 0,
+                        softmax_scale: float | None = None, y=None, workspace=None, stream=None):
+    """Attention of q [T, q_heads, D] (fp16 or bf16) over a KV4Cache -> y [T,
+    q_heads, D]. page_table int32 [B, max_pages], lengths int32 [B] (tokens in
+    the cache, those of the queries included), query_offsets int32 [B + 1] (or
+    T / B query rows per sequence), all on the GPU. Queries stand at the end of
+    their sequences; with causal each sees the tokens up to its own, with a
+    window only the last `window` of them. softmax_scale is D^-0.5 if not
+    given. See cider_kv4_attention in include/cider.h."""
+    import torch
+    dev = torch.cuda.current_device()
+    arrays = _cache_args(dev, cache)
+    T, Hq, D = shape = tuple(q.shape)
+    if D != arrays.head_dim:
+        raise ValueError(f"q must have heads of {arrays.head_dim}, got {D}")
+    qr, qh = _need_rows(dev, q, q.dtype, shape, "q")
+    B, max_pages = page_table.shape
+    _need_on(dev, page_table, torch.int32, (B, max_pages), "page_table")
+    _need_on(dev, lengths, torch.int32, (B,), "lengths")
+    offsets = None
+    if query_offsets is not None:
+        _need_on(dev, query_offsets, torch.int32, (B + 1,), "query_offsets")
+        offsets = query_offsets.data_ptr()
+    if not 0 <= window:
+        raise ValueError("window must not be negative")
+    if y is None:
+        y = torch.empty(shape, dtype=q.dtype, device=q.device)
+    else:
+        _need_on(dev, y, q.dtype, shape, "y")
+    need = _attention_workspace_size(T, B, Hq, arrays.kv_heads, D, max_pages * arrays.page_size)
+    if need and workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif workspace is not None and workspace.is_cuda and workspace.get_device() != dev:
+        raise ValueError(f"workspace must be on the current device {dev}, not {workspace.get_device()}")
+    args = Kv4Attention(arrays, q.data_ptr(), page_table.data_ptr(), lengths.data_ptr(), offsets, y.data_ptr(),
+                        *_ws_args(workspace), T, B, max_pages, qr, qh, _fp_code(q, "q"), Hq, 1 if causal else 0,
+                        min(window, _I32 - 1), D ** -0.5 if softmax_scale is None else softmax_scale)
+    st = lib().cider_kv4_attention(ctypes.byref(args), _raw_stream(stream, dev))
+    if st:
+        _check("cider_kv4_attention", st)
+    return y
+
+
+@_on_stream
+def w8a8_attention(x_q, x_scale, w_qkv, qkv_scale, w_out, out_scale, cache, slots, page_table, lengths, q_heads: int,
+                   query_offsets=None, positions=None, inv_freq=None, interleaved: bool = False, rope_scale: float = 1.0,
+                   q_norm=None, k_norm=None, eps: float = 1e-6, causal: bool = True, window: int = 0,
+                   softmax_scale: float | None = None, out_dtype=None, stream=None):
+    """The attention of a block on the tokens' codes (from cider_norm_quant or
+    cider_quant_act): w_qkv int8 [(q_heads + 2 kv_heads) * D, K], w_out [N,
+    q_heads * D], both with fp32 scales per row. The tokens' keys and values go
+    into the cache at `slots`, lengths count them, and the result [T, N] is the
+    block's output, which cider_norm_quant adds to the residual."""
+    import torch
+    t = out_dtype or torch.float16
+    T, Hkv, D = x_q.shape[0], cache.k_codes.shape[1], 2 * cache.k_codes.shape[3]
+    q, k, v = cider_w8a8_gemm_split(x_q, x_scale, w_qkv, qkv_scale, [q_heads * D, Hkv * D, Hkv * D], stream=stream,
+                                    out_dtype=t)
+    q = q.view(T, q_heads, D)
+    cider_kv4_append(cache, k.view(T, Hkv, D), v.view(T, Hkv, D), slots, q=q, positions=positions, inv_freq=inv_freq,
+                     interleaved=interleaved, rope_scale=rope_scale, q_norm=q_norm, k_norm=k_norm, eps=eps, q_out=q,
+                     stream=stream)
+    a = cider_kv4_attention(q, cache, page_table, lengths, query_offsets=query_offsets, causal=causal, window=window,
+                            softmax_scale=softmax_scale, stream=stream)
+    a_q, a_scale = cider_quant_act(a.view(T, q_heads * D), 0, stream=stream)
+    return cider_w8a8_gemm(a_q, a_scale, w_out, out_scale, 0, stream=stream, out_dtype=t)
 
 
 def cider_stack_workspace_layout(M: int, hidden: int, q_dim: int, kv_dim: int, mlp_dim: int):

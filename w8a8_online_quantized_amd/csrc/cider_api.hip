@@ -704,4 +704,162 @@ cider_status_t cider_dequant_act(const int8_t* x_q, const float* x_scale, int64_
                                              static_cast<hipStream_t>(stream)));
 }
 
+// ---- attention blocks -------------------------------------------------------
+
+static bool kv4_cache_ok(const cider_kv4_cache_t& c) {
+  if (c.head_dim != 64 && c.head_dim != 128 && c.head_dim != 256) return false;
+  const int32_t gs = c.group_size ? c.group_size : c.head_dim;
+  if (gs < 32 || (gs != c.head_dim && 2 * gs != c.head_dim && 4 * gs != c.head_dim)) return false;
+  if (c.page_size < 16 || c.page_size > CIDER_KV4_MAX_PAGE_SIZE || (c.page_size & (c.page_size - 1))) return false;
+  if (c.kv_heads < 1 || c.kv_heads > CIDER_KV4_MAX_HEADS || c.n_pages < 1) return false;
+  return c.n_pages < (int64_t(1) << 31) / c.page_size;   // slots are int32
+}
+
+static bool kv4_cache_there(const cider_kv4_cache_t& c) {
+  return c.k_codes && c.k_scale && c.v_codes && c.v_scale && aligned16(c.k_codes) && aligned16(c.k_scale) &&
+         aligned16(c.v_codes) && aligned16(c.v_scale);
+}
+
+static cider::Kv4Cache kv4_cache_of(const cider_kv4_cache_t& c) {
+  int shift = 0;
+  while ((1 << shift) < c.page_size) ++shift;
+  return cider::Kv4Cache{c.k_codes,   c.k_scale, c.v_codes,  c.v_scale,  c.n_pages,
+                         c.page_size, shift,     c.kv_heads, c.head_dim, c.group_size ? c.head_dim / c.group_size : 1};
+}
+
+// Strides of a [T, heads, D] array that is written: no two elements in one place.
+static bool rows_apart(int64_t T, int64_t heads, int64_t D, int64_t row, int64_t head) {
+  constexpr int64_t kMost = int64_t(1) << 40;
+  if (row < 0 || head < 0 || row > kMost || head > kMost) return false;
+  return ((heads == 1 || head >= D) && (T == 1 || row >= (heads - 1) * head + D)) ||
+         ((T == 1 || row >= D) && (heads == 1 || head >= (T - 1) * row + D));
+}
+
+static bool strides_ok(int64_t row, int64_t head) {   // of an array that is read
+  constexpr int64_t kMost = int64_t(1) << 40;
+  return row >= 0 && head >= 0 && row <= kMost && head <= kMost;
+}
+
+cider_status_t cider_rope(const cider_rope_t* args, void* stream) {
+  if (!args) return CIDER_ERROR_INVALID_VALUE;
+  const cider_rope_t& a = *args;
+  // one workgroup of 256 threads per token and slice of heads: the grid stays below 2^31 threads
+  if (!valid_dtype(a.dtype) || a.T < 0 || a.T >= (int64_t(1) << 23) || a.heads < 0 || a.head_dim < 2 ||
+      a.head_dim > CIDER_ROPE_MAX_HEAD_DIM || a.heads > CIDER_ROPE_MAX_HEADS)
+    return CIDER_ERROR_INVALID_VALUE;
+  if (a.rotary_dim < 2 || a.rotary_dim % 2 || a.rotary_dim > a.head_dim || a.rotary_dim > CIDER_ROPE_MAX_ROTARY_DIM ||
+      (a.interleaved != 0 && a.interleaved != 1) || !std::isfinite(a.scale))
+    return CIDER_ERROR_INVALID_VALUE;
+  if (a.T == 0 || a.heads == 0) return CIDER_SUCCESS;
+  if (!a.x || !a.y || !a.positions || !a.inv_freq) return CIDER_ERROR_INVALID_VALUE;
+  if (!strides_ok(a.x_row_stride, a.x_head_stride) ||
+      !rows_apart(a.T, a.heads, a.head_dim, a.y_row_stride, a.y_head_stride) ||
+      (a.x == a.y && (a.x_row_stride != a.y_row_stride || a.x_head_stride != a.y_head_stride)))
+    return CIDER_ERROR_INVALID_VALUE;
+  for (const void* p : {a.x, static_cast<const void*>(a.y), static_cast<const void*>(a.positions),
+                        static_cast<const void*>(a.inv_freq)})
+    if (!aligned16(p)) return CIDER_ERROR_INVALID_VALUE;
+  const cider::RopeArgs r{a.x,      a.y,     a.positions, a.inv_freq, a.T,          a.x_row_stride, a.x_head_stride,
+                          a.y_row_stride, a.y_head_stride, a.heads,   a.head_dim,   a.rotary_dim,   a.interleaved,
+                          a.scale};
+  if (!cider::rope_fits(r)) return CIDER_ERROR_INVALID_VALUE;
+  if (!device_is_gfx950()) return CIDER_ERROR_NOT_SUPPORTED;
+  return from_hip(cider::launch_rope(r, a.dtype == CIDER_DTYPE_BF16, static_cast<hipStream_t>(stream)));
+}
+
+cider_status_t cider_kv4_append(const cider_kv4_append_t* args, void* stream) {
+  if (!args) return CIDER_ERROR_INVALID_VALUE;
+  const cider_kv4_append_t& a = *args;
+  const cider_kv4_cache_t& c = a.cache;
+  if (!kv4_cache_ok(c) || !valid_dtype(a.dtype) || a.T < 0 || a.T >= (int64_t(1) << 23) || a.q_heads < 0 ||
+      a.q_heads > CIDER_KV4_MAX_Q_HEADS)
+    return CIDER_ERROR_INVALID_VALUE;
+  if (a.T == 0) return CIDER_SUCCESS;
+  if ((a.q != nullptr) != (a.q_out != nullptr) || (a.q == nullptr && a.q_norm != nullptr) ||
+      (a.positions != nullptr) != (a.inv_freq != nullptr))
+    return CIDER_ERROR_INVALID_VALUE;
+  if (a.positions && (a.rotary_dim < 16 || a.rotary_dim % 16 || a.rotary_dim > c.head_dim ||
+                      (a.interleaved != 0 && a.interleaved != 1) || !std::isfinite(a.rope_scale)))
+    return CIDER_ERROR_INVALID_VALUE;
+  if ((a.q_norm || a.k_norm) && (!std::isfinite(a.eps) || !(a.eps > 0.0f))) return CIDER_ERROR_INVALID_VALUE;
+  if (!kv4_cache_there(c) || !a.k || !a.v || !a.slots || (a.q && a.q_heads < 1)) return CIDER_ERROR_INVALID_VALUE;
+  for (const int64_t s : {a.q_row_stride, a.q_head_stride, a.k_row_stride, a.k_head_stride, a.v_row_stride,
+                          a.v_head_stride, a.out_row_stride, a.out_head_stride})
+    if (s % 8) return CIDER_ERROR_INVALID_VALUE;
+  if (!strides_ok(a.k_row_stride, a.k_head_stride) || !strides_ok(a.v_row_stride, a.v_head_stride))
+    return CIDER_ERROR_INVALID_VALUE;
+  if (a.q && (!strides_ok(a.q_row_stride, a.q_head_stride) ||
+              !rows_apart(a.T, a.q_heads, c.head_dim, a.out_row_stride, a.out_head_stride) ||
+              (a.q == a.q_out && (a.q_row_stride != a.out_row_stride || a.q_head_stride != a.out_head_stride))))
+    return CIDER_ERROR_INVALID_VALUE;
+  for (const void* p : {a.q, a.k, a.v, a.q_norm, a.k_norm, static_cast<const void*>(a.positions),
+                        static_cast<const void*>(a.inv_freq), static_cast<const void*>(a.slots),
+                        static_cast<const void*>(a.q_out)})
+    if (!aligned16(p)) return CIDER_ERROR_INVALID_VALUE;
+  if (!device_is_gfx950()) return CIDER_ERROR_NOT_SUPPORTED;
+  const cider::Kv4AppendArgs k{kv4_cache_of(c), a.q, a.k, a.v, a.q_norm, a.k_norm, a.positions, a.inv_freq, a.slots,
+                               a.q_out, a.T, a.q_row_stride, a.q_head_stride, a.k_row_stride, a.k_head_stride,
+                               a.v_row_stride, a.v_head_stride, a.out_row_stride, a.out_head_stride,
+                               a.q ? a.q_heads : 0, a.rotary_dim, a.interleaved, a.rope_scale, a.eps};
+  return from_hip(cider::launch_kv4_append(k, a.dtype == CIDER_DTYPE_BF16, static_cast<hipStream_t>(stream)));
+}
+
+cider_status_t cider_kv4_read(const cider_kv4_cache_t* cache, const int32_t* slots, int64_t n, void* k, void* v,
+                              int32_t dtype, void* stream) {
+  if (!cache || !kv4_cache_ok(*cache) || !valid_dtype(dtype) || n < 0 || n >= (int64_t(1) << 31))
+    return CIDER_ERROR_INVALID_VALUE;
+  if (n == 0) return CIDER_SUCCESS;
+  if (!kv4_cache_there(*cache) || !slots || !k || !v || !aligned16(slots) || !aligned16(k) || !aligned16(v))
+    return CIDER_ERROR_INVALID_VALUE;
+  if (!device_is_gfx950()) return CIDER_ERROR_NOT_SUPPORTED;
+  return from_hip(cider::launch_kv4_read(kv4_cache_of(*cache), slots, n, k, v, dtype == CIDER_DTYPE_BF16,
+                                         static_cast<hipStream_t>(stream)));
+}
+
+static bool kv4_attention_sizes_ok(int64_t T, int64_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                   int64_t capacity) {
+  constexpr int64_t kLimit = int64_t(1) << 31;
+  if (T < 0 || T >= kLimit || B < 1 || B >= kLimit || capacity < 0 || capacity >= kLimit || kv_heads < 1 ||
+      kv_heads > CIDER_KV4_MAX_HEADS || q_heads < 1 || q_heads > CIDER_KV4_MAX_Q_HEADS || q_heads % kv_heads)
+    return false;
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return false;
+  return T == 0 || (T * q_heads < kLimit && cider::kv4_attention_fits(T, B, q_heads, kv_heads, head_dim, capacity));
+}
+
+int64_t cider_kv4_attention_workspace_size(int64_t T, int64_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                           int64_t capacity) {
+  if (!kv4_attention_sizes_ok(T, B, q_heads, kv_heads, head_dim, capacity)) return -1;
+  return T == 0 ? 0 : cider::kv4_attention_workspace_bytes(T, B, q_heads, kv_heads, head_dim, capacity);
+}
+
+cider_status_t cider_kv4_attention(const cider_kv4_attention_t* args, void* stream) {
+  if (!args) return CIDER_ERROR_INVALID_VALUE;
+  const cider_kv4_attention_t& a = *args;
+  const cider_kv4_cache_t& c = a.cache;
+  if (!kv4_cache_ok(c) || !valid_dtype(a.dtype) || a.max_pages < 0 || a.max_pages >= (int64_t(1) << 31))
+    return CIDER_ERROR_INVALID_VALUE;
+  const int64_t capacity = a.max_pages * c.page_size;
+  if (!kv4_attention_sizes_ok(a.T, a.B, a.q_heads, c.kv_heads, c.head_dim, capacity)) return CIDER_ERROR_INVALID_VALUE;
+  if ((a.causal != 0 && a.causal != 1) || a.window < 0 || !std::isfinite(a.softmax_scale) ||
+      (!a.query_offsets && a.T % a.B))
+    return CIDER_ERROR_INVALID_VALUE;
+  if (a.T == 0) return CIDER_SUCCESS;
+  if (!kv4_cache_there(c) || !a.q || !a.y || !a.lengths || (a.max_pages && !a.page_table)) return CIDER_ERROR_INVALID_VALUE;
+  if (!strides_ok(a.q_row_stride, a.q_head_stride) || a.q_row_stride % 8 || a.q_head_stride % 8)
+    return CIDER_ERROR_INVALID_VALUE;
+  for (const void* p : {a.q, static_cast<const void*>(a.page_table), static_cast<const void*>(a.lengths),
+                        static_cast<const void*>(a.query_offsets), static_cast<const void*>(a.y),
+                        static_cast<const void*>(a.workspace)})
+    if (!aligned16(p)) return CIDER_ERROR_INVALID_VALUE;
+  const int64_t need = cider::kv4_attention_workspace_bytes(a.T, a.B, a.q_heads, c.kv_heads, c.head_dim, capacity);
+  if (need > 0 && (!a.workspace || a.workspace_bytes < need)) return CIDER_ERROR_INVALID_VALUE;
+  if (!device_is_gfx950()) return CIDER_ERROR_NOT_SUPPORTED;
+  // a window that reaches over the whole capacity hides nothing
+  const cider::Kv4AttentionArgs k{kv4_cache_of(c), a.q, a.page_table, a.lengths, a.query_offsets, a.y,
+                                  static_cast<float*>(a.workspace), a.T, a.B, a.max_pages, a.q_row_stride,
+                                  a.q_head_stride, a.q_heads, a.causal, a.window < capacity ? a.window : 0,
+                                  a.softmax_scale};
+  return from_hip(cider::launch_kv4_attention(k, a.dtype == CIDER_DTYPE_BF16, static_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"

@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "cider_kv4.h"
+
 namespace cider {
 
 // Launches the activation / weight quantization kernel.
@@ -137,5 +139,59 @@ hipError_t launch_norm(const NormArgs& args, bool bf16, hipStream_t stream);
 // y [M, K] = codes [M, K] times their scales (group_size as for quantizing).
 hipError_t launch_dequant_rows(const int8_t* q, const float* s, int64_t M, int64_t K, int group_size, void* y,
                                bool bf16, hipStream_t stream);
+
+// Rotary positions: x, y [T, heads, head_dim] with strides in elements.
+struct RopeArgs {
+  const void* x;
+  void* y;
+  const int32_t* positions;   // [T]
+  const double* inv_freq;     // [rotary_dim / 2]
+  int64_t T, x_row_stride, x_head_stride, y_row_stride, y_head_stride;
+  int heads, head_dim, rotary_dim, interleaved;
+  float scale;
+};
+bool rope_fits(const RopeArgs& args);   // whether the grid stays below 2^31 threads
+hipError_t launch_rope(const RopeArgs& args, bool bf16, hipStream_t stream);
+
+// Keys and values into the 4-bit cache, with what happens to q and k before.
+struct Kv4AppendArgs {
+  Kv4Cache cache;
+  const void* q;              // [T, q_heads, D] or null
+  const void* k;              // [T, kv_heads, D]
+  const void* v;
+  const void* q_norm;         // [D] or null
+  const void* k_norm;
+  const int32_t* positions;   // [T] or null: no rotation
+  const double* inv_freq;     // [rotary_dim / 2]
+  const int32_t* slots;       // [T]
+  void* q_out;
+  int64_t T, q_row_stride, q_head_stride, k_row_stride, k_head_stride, v_row_stride, v_head_stride, out_row_stride,
+      out_head_stride;
+  int q_heads, rotary_dim, interleaved;
+  float rope_scale, eps;
+};
+hipError_t launch_kv4_append(const Kv4AppendArgs& args, bool bf16, hipStream_t stream);
+
+// k, v [n, kv_heads, D] = the cache's rows at slots (zeros outside the cache).
+hipError_t launch_kv4_read(const Kv4Cache& cache, const int32_t* slots, int64_t n, void* k, void* v, bool bf16,
+                           hipStream_t stream);
+
+// Attention over the cache's pages.
+struct Kv4AttentionArgs {
+  Kv4Cache cache;
+  const void* q;                 // [T, q_heads, D], strides in elements
+  const int32_t* page_table;     // [B, max_pages]
+  const int32_t* lengths;        // [B]
+  const int32_t* query_offsets;  // [B + 1], or null: T / B queries each
+  void* y;                       // [T, q_heads, D]
+  float* workspace;              // kv4_attention_workspace_bytes
+  int64_t T, B, max_pages, q_row_stride, q_head_stride;
+  int q_heads, causal, window;   // window 0: none
+  float softmax_scale;
+};
+// Sizes whose grid of workgroups fits a launch.
+bool kv4_attention_fits(int64_t T, int64_t B, int q_heads, int kv_heads, int head_dim, int64_t capacity);
+int64_t kv4_attention_workspace_bytes(int64_t T, int64_t B, int q_heads, int kv_heads, int head_dim, int64_t capacity);
+hipError_t launch_kv4_attention(const Kv4AttentionArgs& args, bool bf16, hipStream_t stream);
 
 }  // namespace cider
