@@ -155,7 +155,7 @@ struct Raw {                            // 32 tokens as loaded
 };
 
 template <int D, int G, bool BF, int NQ, bool SPLIT>
-__global__ void __launch_bounds__(kThreads) kv4_attention(Kv4AttentionArgs a, Plan plan) {
+__global__ void __launch_bounds__(kThreads, 2) kv4_attention(Kv4AttentionArgs a, Plan plan) {
   constexpr int kTiles = D / 16;        // output tiles of 16 dimensions; also the codes of a sixteenth
   constexpr int kPer = kTiles / G;      // of one group
   constexpr int kSteps = D / 32;        // products of one score
@@ -276,14 +276,18 @@ __global__ void __launch_bounds__(kThreads) kv4_attention(Kv4AttentionArgs a, Pl
   const int32_t* table = a.page_table + b * a.max_pages;
   const int page_size = a.cache.page_size, page_shift = a.cache.page_shift;
 
-  // page of a sub-tile of 16 tokens, -1 where there is nothing to read
-  auto page_of = [&](int t) {
+  // The pages of 64 sub-tiles of 16 tokens from the wave's step `first` on (a
+  // lane each, -1 where there is nothing to read), so that the steps' loads wait
+  // for no table entry.
+  constexpr int kStride = SPLIT ? kWaves : 1;
+  auto pages_from = [&](int first) {
+    const int t = first_token + (first + (lane >> 1) * kStride) * kTokens + (lane & 1) * 16;
     int p = -1;
     if (t < any_hi) {
       p = table[t >> page_shift];
       if (p < 0 || p >= a.cache.n_pages) p = -1;
     }
-    return uniform(p);
+    return p;
   };
   using R = Raw<D, G>;
   auto load = [&](int t, const int (&pages)[2], R& r) {
@@ -471,7 +475,6 @@ __global__ void __launch_bounds__(kThreads) kv4_attention(Kv4AttentionArgs a, Pl
 
   // ---- the tokens, the next step's codes on their way during each step
   {
-    constexpr int kStride = SPLIT ? kWaves : 1;
     int step = part * sh.per + (SPLIT ? wave : 0);
     int stop = step_end;
     if constexpr (!SPLIT) {
@@ -480,26 +483,30 @@ __global__ void __launch_bounds__(kThreads) kv4_attention(Kv4AttentionArgs a, Pl
       step = max(step, (any_lo - first_token) / kTokens);
     }
     auto token = [&](int s) { return first_token + s * kTokens; };
-    auto pages_at = [&](int s, int (&p)[2]) {
-      p[0] = s < stop ? page_of(token(s)) : -1;
-      p[1] = s < stop ? page_of(token(s) + 16) : -1;
-    };
     if (step < stop) {
+      int ids = pages_from(step), at = 0;         // `at`: the sub-tile of ids that comes next
+      auto take = [&](int (&p)[2]) {
+        p[0] = __builtin_amdgcn_readlane(ids, at);
+        p[1] = __builtin_amdgcn_readlane(ids, at + 1);
+        at += 2;
+      };
       int pages[2], next[2];
       R cur, nxt;
-      pages_at(step, pages);
+      take(pages);
       load(token(step), pages, cur);
-      pages_at(step + kStride, next);
       for (; step < stop; step += kStride) {
-        int after[2];
-        pages_at(step + 2 * kStride, after);
-        if (step + kStride < stop) load(token(step + kStride), next, nxt);
+        if (step + kStride < stop) {
+          if (at == 64) {
+            ids = pages_from(step + kStride);
+            at = 0;
+          }
+          take(next);
+          load(token(step + kStride), next, nxt);
+        }
         process(token(step), pages, cur);
         cur = nxt;
         pages[0] = next[0];
         pages[1] = next[1];
-        next[0] = after[0];
-        next[1] = after[1];
       }
     }
   }
@@ -616,14 +623,16 @@ __global__ void __launch_bounds__(kThreads) kv4_attention(Kv4AttentionArgs a, Pl
   }
 }
 
-// The parts of each row, joined: D / 8 lanes per row.
+// The parts of each row, joined. One workgroup per row: D / 8 lanes hold its
+// dimensions, and the workgroup's slices take the parts in turn.
+constexpr int kMaxParts = kThreads;
+
 template <int D, bool BF>
 __global__ void __launch_bounds__(kThreads) kv4_join(Kv4AttentionArgs a, Plan plan) {
-  constexpr int kLanes = D / 8;
-  const int64_t row = (int64_t)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
-  const int c = threadIdx.x % kLanes;
-  const int64_t all_rows = a.T * a.q_heads;
-  if (row >= all_rows) return;
+  constexpr int kLanes = D / 8, kSlices = kThreads / kLanes;
+  __shared__ float weight[kMaxParts], wave_top[kWaves], wave_sum[kWaves];
+  __shared__ float slice_o[kSlices][D];
+  const int64_t row = blockIdx.x, all_rows = a.T * a.q_heads;
   const int64_t token = row / a.q_heads;
   const int head = (int)(row - token * a.q_heads), heads = a.q_heads / a.cache.kv_heads;
   int64_t b;
@@ -645,24 +654,58 @@ __global__ void __launch_bounds__(kThreads) kv4_join(Kv4AttentionArgs a, Plan pl
   const int last = min(rows, row0 + plan.rows) - 1;
   const Share sh = share(a, seq, row0 / heads, last / heads, plan.parts, plan.least);
   if (sh.parts == 1) return;            // written by its workgroup
-  const float* ml = a.workspace + plan.parts * all_rows * D;
-  float top = kLeast;
-  for (int p = 0; p < sh.parts; ++p) top = __builtin_fmaxf(top, ml[(p * all_rows + row) * 2]);
-  float sum = 0.0f, out[8];
+  const int c = threadIdx.x % kLanes, slice = threadIdx.x / kLanes, wave = threadIdx.x >> 6;
+
+  float m = kLeast, l = 0.0f;
+  if ((int)threadIdx.x < sh.parts) {
+    const float2 ml = reinterpret_cast<const float2*>(a.workspace + plan.parts * all_rows * D)[threadIdx.x * all_rows + row];
+    m = ml.x;
+    l = ml.y;
+  }
+  float top = m;
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, off));
+  if ((threadIdx.x & 63) == 0) wave_top[wave] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) top = __builtin_fmaxf(top, wave_top[w]);
+  const float f = __builtin_amdgcn_exp2f(m - top) * l;
+  float sum = f;
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off);
+  if ((threadIdx.x & 63) == 0) wave_sum[wave] = sum;
+  weight[threadIdx.x] = f;
+  __syncthreads();
+  sum = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) sum += wave_sum[w];
+
+  float out[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) out[e] = 0.0f;
-  for (int p = 0; p < sh.parts; ++p) {
-    const float f = __builtin_amdgcn_exp2f(ml[(p * all_rows + row) * 2] - top) * ml[(p * all_rows + row) * 2 + 1];
+#pragma unroll 2
+  for (int p = slice; p < sh.parts; p += kSlices) {
     const float* po = a.workspace + (p * all_rows + row) * D + 8 * c;
     const f4 u = *reinterpret_cast<const f4*>(po), w = *reinterpret_cast<const f4*>(po + 4);
-    sum += f;
-    if (f != 0.0f) {
+    const float g = weight[p];
+    if (g != 0.0f) {                    // a part without a visible token holds nothing
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        out[e] = __builtin_fmaf(f, u[e], out[e]);
-        out[4 + e] = __builtin_fmaf(f, w[e], out[4 + e]);
+        out[e] = __builtin_fmaf(g, u[e], out[e]);
+        out[4 + e] = __builtin_fmaf(g, w[e], out[4 + e]);
       }
     }
+  }
+  const int used = min(kSlices, sh.parts);
+  if (slice > 0 && slice < used) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) slice_o[slice][8 * c + e] = out[e];
+  }
+  __syncthreads();
+  if (slice > 0) return;
+  for (int s = 1; s < used; ++s) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) out[e] += slice_o[s][8 * c + e];
   }
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
@@ -686,7 +729,7 @@ Plan plan_of(int64_t T, int64_t B, int q_heads, int kv_heads, int64_t capacity, 
   p.least = split ? kWaves : 16;
   const int64_t steps = (capacity + kTokens - 1) / kTokens;
   const int64_t groups = std::max<int64_t>(p.slots * kv_heads, 1), want = split ? 2048 : 512;
-  p.parts = (int)std::max<int64_t>(1, std::min<int64_t>({(want + groups - 1) / groups, (steps + p.least - 1) / p.least, 256}));
+  p.parts = (int)std::max<int64_t>(1, std::min<int64_t>({(want + groups - 1) / groups, (steps + p.least - 1) / p.least, kMaxParts}));
   return p;
 }
 
@@ -696,8 +739,7 @@ void launch_attention_t(const Kv4AttentionArgs& a, const Plan& p, hipStream_t st
   if (p.rows == 16) kv4_attention<D, G, BF, 1, true><<<grid, block, 0, st>>>(a, p);
   else kv4_attention<D, G, BF, kPrefillTiles, false><<<grid, block, 0, st>>>(a, p);
   if (p.parts > 1) {
-    constexpr int kRows = kThreads / (D / 8);
-    kv4_join<D, BF><<<dim3((unsigned)((a.T * a.q_heads + kRows - 1) / kRows)), block, 0, st>>>(a, p);
+    kv4_join<D, BF><<<dim3((unsigned)(a.T * a.q_heads)), block, 0, st>>>(a, p);
   }
 }
 
@@ -717,12 +759,13 @@ void launch_attention_d(const Kv4AttentionArgs& a, const Plan& p, hipStream_t st
 
 }  // namespace
 
-bool kv4_attention_fits(int64_t T, int64_t B, int q_heads, int kv_heads, int head_dim, int64_t capacity) {
+bool kv4_attention_fits(int64_t T, int64_t B, int q_heads, int kv_heads, int64_t capacity) {
   for (const bool ragged : {false, true}) {
     const Plan p = plan_of(T, B, q_heads, kv_heads, capacity, ragged);
     if (p.slots * p.parts * kv_heads * kThreads >= (int64_t(1) << 31)) return false;
+    if (p.parts > 1 && T * q_heads * kThreads >= (int64_t(1) << 31)) return false;
   }
-  return T * q_heads * (head_dim / 8) < (int64_t(1) << 31);
+  return true;
 }
 
 int64_t kv4_attention_workspace_bytes(int64_t T, int64_t B, int q_heads, int kv_heads, int head_dim, int64_t capacity) {
