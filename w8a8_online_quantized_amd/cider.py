@@ -14,6 +14,7 @@ import functools
 import math
 import os
 import re
+import struct
 import typing
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -141,6 +142,28 @@ class Kv4Attention(ctypes.Structure):
                [(n, ctypes.c_int32) for n in ("dtype", "q_heads", "causal", "window")] + \
                [("softmax_scale", ctypes.c_float)]
 
+
+def _packer(cls):
+    """A function that packs a structure's values, in the order of its fields
+    (nested ones in place, 0 for no pointer), into bytes that a C call takes by
+    address: a third of the time of filling the ctypes structure, and numbers
+    that do not fit their field raise instead of being taken modulo 2^32."""
+    def codes(c):
+        letter = {ctypes.c_void_p: "P", ctypes.c_int64: "q", ctypes.c_int32: "i", ctypes.c_float: "f"}
+        return "".join(letter[t] if t in letter else codes(t) for _, t in c._fields_)
+    form = struct.Struct(codes(cls))
+    form = struct.Struct(f"{codes(cls)}{ctypes.sizeof(cls) - form.size}x")
+    assert form.size == ctypes.sizeof(cls)
+
+    def pack(*values):
+        try:
+            return form.pack(*values)
+        except (struct.error, OverflowError) as e:
+            raise ValueError(f"{cls.__doc__.split()[0].rstrip('.:')}: {e}") from None
+    return pack
+
+
+_pack_rope, _pack_cache, _pack_append, _pack_attention = map(_packer, (Rope, Kv4CacheArrays, Kv4Append, Kv4Attention))
 
 _lib = None
 
@@ -913,46 +936,50 @@ def _need_rows(dev, t, dtype, shape, name):
     """A [T, heads, D] tensor on the current device whose heads are contiguous:
     its (row, head) strides. A dimension of one has a stride of its own."""
     import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.get_device() != dev:
+    try:
+        fits = t.dtype is dtype and t.shape == shape and t.get_device() == dev
+    except AttributeError:
+        fits = False
+    if not fits:
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
         raise ValueError(f"{name} must be on the current device {dev}, not {t.get_device()}")
     T, H, D = shape
     row, head, one = t.stride()
     if one != 1 and D > 1:
         raise ValueError(f"{name} must have contiguous heads")
-    head = head if H > 1 else D
+    if H == 1:
+        head = D
     return (row if T > 1 else H * D), head
 
 
 def _cache_args(dev, cache):
+    """The values of cider_kv4_cache_t."""
     import torch
-    k_codes = cache.k_codes
-    n_pages, hkv, page, half = k_codes.shape
-    G = cache.k_scale.shape[2]
-    codes, scales = (n_pages, hkv, page, half), (n_pages, hkv, G, page)
+    k_codes, k_scale, v_codes, v_scale = cache
+    n_pages, hkv, page, half = codes = k_codes.shape
+    G = k_scale.shape[2]
+    scales = (n_pages, hkv, G, page)
     _need_on(dev, k_codes, torch.uint8, codes, "k_codes")
-    _need_on(dev, cache.v_codes, torch.uint8, codes, "v_codes")
-    _need_on(dev, cache.k_scale, torch.float32, scales, "k_scale")
-    _need_on(dev, cache.v_scale, torch.float32, scales, "v_scale")
+    _need_on(dev, v_codes, torch.uint8, codes, "v_codes")
+    _need_on(dev, k_scale, torch.float32, scales, "k_scale")
+    _need_on(dev, v_scale, torch.float32, scales, "v_scale")
     D = 2 * half
-    if not G or D % G or max(page, hkv, D) >= _I32:
+    if not G or D % G:
         raise ValueError("the cache's groups must divide its heads")
-    return Kv4CacheArrays(k_codes.data_ptr(), cache.k_scale.data_ptr(), cache.v_codes.data_ptr(), cache.v_scale.data_ptr(),
-                          n_pages, page, hkv, D, D // G)
+    return (k_codes.data_ptr(), k_scale.data_ptr(), v_codes.data_ptr(), v_scale.data_ptr(), n_pages, page, hkv, D, D // G)
 
 
 def _rotation(dev, T, positions, inv_freq):
     import torch
+    n = inv_freq.numel()
     _need_on(dev, positions, torch.int32, (T,), "positions")
-    _need_on(dev, inv_freq, torch.float64, (inv_freq.numel(),), "inv_freq")
-    if 2 * inv_freq.numel() >= _I32:
-        raise ValueError("too many frequencies")
-    return positions.data_ptr(), inv_freq.data_ptr(), 2 * inv_freq.numel()
+    _need_on(dev, inv_freq, torch.float64, (n,), "inv_freq")
+    return positions.data_ptr(), inv_freq.data_ptr(), 2 * n
 
 
 @_on_stream
@@ -964,15 +991,17 @@ def cider_rope(x, positions, inv_freq, interleaved: bool = False, scale: float =
     inv_freq and scale."""
     import torch
     dev = torch.cuda.current_device()
-    T, H, D = shape = tuple(x.shape)
-    xr, xh = _need_rows(dev, x, x.dtype, shape, "x")
+    T, H, D = shape = x.shape
+    t = x.dtype
+    xr, xh = _need_rows(dev, x, t, shape, "x")
     pos, freq, rd = _rotation(dev, T, positions, inv_freq)
     if y is None:
-        y = torch.empty(shape, dtype=x.dtype, device=x.device)
-    yr, yh = _need_rows(dev, y, x.dtype, shape, "y")
-    args = Rope(x.data_ptr(), pos, freq, y.data_ptr(), T, xr, xh, yr, yh, _fp_code(x, "x"), min(H, _I32 - 1),
-                min(D, _I32 - 1), rd, 1 if interleaved else 0, scale)
-    st = lib().cider_rope(ctypes.byref(args), _raw_stream(stream, dev))
+        y, yr, yh = torch.empty(T, H, D, dtype=t, device=x.device), H * D, D
+    else:
+        yr, yh = _need_rows(dev, y, t, shape, "y")
+    args = _pack_rope(x.data_ptr(), pos, freq, y.data_ptr(), T, xr, xh, yr, yh, _fp_code(x, "x"), H, D, rd,
+                      1 if interleaved else 0, scale)
+    st = lib().cider_rope(args, _raw_stream(stream, dev))
     if st:
         _check("cider_rope", st)
     return y
@@ -990,20 +1019,21 @@ def cider_kv4_append(cache, k, v, slots, q=None, positions=None, inv_freq=None, 
     import torch
     dev = torch.cuda.current_device()
     arrays = _cache_args(dev, cache)
-    T, t, D, Hkv = k.shape[0], k.dtype, arrays.head_dim, arrays.kv_heads
-    kr, kh = _need_rows(dev, k, t, (T, Hkv, D), "k")
-    vr, vh = _need_rows(dev, v, t, (T, Hkv, D), "v")
+    T, Hkv, D, t = k.shape[0], arrays[6], arrays[7], k.dtype
+    rows = (T, Hkv, D)
+    kr, kh = _need_rows(dev, k, t, rows, "k")
+    vr, vh = _need_rows(dev, v, t, rows, "v")
     _need_on(dev, slots, torch.int32, (T,), "slots")
-    pq = pqn = pkn = pos = freq = po = None
+    pq = pqn = pkn = pos = freq = po = 0
     qr = qh = our = ouh = Hq = rd = 0
     if q is not None:
         Hq = q.shape[1]
-        if Hq >= _I32:
-            raise ValueError("too many query heads")
-        qr, qh = _need_rows(dev, q, t, (T, Hq, D), "q")
+        rows = (T, Hq, D)
+        qr, qh = _need_rows(dev, q, t, rows, "q")
         if q_out is None:
-            q_out = torch.empty(T, Hq, D, dtype=t, device=q.device)
-        our, ouh = _need_rows(dev, q_out, t, (T, Hq, D), "q_out")
+            q_out, our, ouh = torch.empty(T, Hq, D, dtype=t, device=q.device), Hq * D, D
+        else:
+            our, ouh = _need_rows(dev, q_out, t, rows, "q_out")
         pq, po = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None or q_norm is not None:
         raise ValueError("q_out and q_norm need q")
@@ -1019,9 +1049,9 @@ def cider_kv4_append(cache, k, v, slots, q=None, positions=None, inv_freq=None, 
         pos, freq, rd = _rotation(dev, T, positions, inv_freq)
     elif inv_freq is not None:
         raise ValueError("inv_freq needs positions")
-    args = Kv4Append(arrays, pq, k.data_ptr(), v.data_ptr(), pqn, pkn, pos, freq, slots.data_ptr(), po, T, qr, qh, kr, kh,
-                     vr, vh, our, ouh, _fp_code(k, "k"), Hq, rd, 1 if interleaved else 0, rope_scale, eps)
-    st = lib().cider_kv4_append(ctypes.byref(args), _raw_stream(stream, dev))
+    args = _pack_append(*arrays, pq, k.data_ptr(), v.data_ptr(), pqn, pkn, pos, freq, slots.data_ptr(), po, T, qr, qh, kr,
+                        kh, vr, vh, our, ouh, _fp_code(k, "k"), Hq, rd, 1 if interleaved else 0, rope_scale, eps)
+    st = lib().cider_kv4_append(args, _raw_stream(stream, dev))
     if st:
         _check("cider_kv4_append", st)
     return q_out
@@ -1035,17 +1065,17 @@ def cider_kv4_read(cache, slots, k=None, v=None, stream=None, out_dtype=None):
     dev = torch.cuda.current_device()
     arrays = _cache_args(dev, cache)
     n = slots.numel()
-    shape = (n, arrays.kv_heads, arrays.head_dim)
+    shape = (n, arrays[6], arrays[7])
     _need_on(dev, slots, torch.int32, (n,), "slots")
     if k is None:
-        k = torch.empty(shape, dtype=out_dtype or (v.dtype if v is not None else torch.float16), device=slots.device)
+        k = torch.empty(*shape, dtype=out_dtype or (v.dtype if v is not None else torch.float16), device=slots.device)
     else:
         _need_on(dev, k, k.dtype, shape, "k")
     if v is None:
         v = torch.empty_like(k)
     else:
         _need_on(dev, v, k.dtype, shape, "v")
-    st = lib().cider_kv4_read(ctypes.byref(arrays), slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), _fp_code(k, "k"),
+    st = lib().cider_kv4_read(_pack_cache(*arrays), slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), _fp_code(k, "k"),
                               _raw_stream(stream, dev))
     if st:
         _check("cider_kv4_read", st)
@@ -1079,32 +1109,37 @@ def cider_kv4_attention(q, cache, page_table, lengths, query_offsets=None, causa
     import torch
     dev = torch.cuda.current_device()
     arrays = _cache_args(dev, cache)
-    T, Hq, D = shape = tuple(q.shape)
-    if D != arrays.head_dim:
-        raise ValueError(f"q must have heads of {arrays.head_dim}, got {D}")
-    qr, qh = _need_rows(dev, q, q.dtype, shape, "q")
-    B, max_pages = page_table.shape
-    _need_on(dev, page_table, torch.int32, (B, max_pages), "page_table")
+    T, Hq, D = shape = q.shape
+    t = q.dtype
+    if D != arrays[7]:
+        raise ValueError(f"q must have heads of {arrays[7]}, got {D}")
+    qr, qh = _need_rows(dev, q, t, shape, "q")
+    B, max_pages = pages = page_table.shape
+    _need_on(dev, page_table, torch.int32, pages, "page_table")
     _need_on(dev, lengths, torch.int32, (B,), "lengths")
-    offsets = None
+    offsets = 0
     if query_offsets is not None:
         _need_on(dev, query_offsets, torch.int32, (B + 1,), "query_offsets")
         offsets = query_offsets.data_ptr()
-    if not 0 <= window:
+    if window < 0:
         raise ValueError("window must not be negative")
     if y is None:
-        y = torch.empty(shape, dtype=q.dtype, device=q.device)
+        y = torch.empty(T, Hq, D, dtype=t, device=q.device)
     else:
-        _need_on(dev, y, q.dtype, shape, "y")
-    need = _attention_workspace_size(T, B, Hq, arrays.kv_heads, D, max_pages * arrays.page_size)
-    if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    elif workspace is not None and workspace.is_cuda and workspace.get_device() != dev:
-        raise ValueError(f"workspace must be on the current device {dev}, not {workspace.get_device()}")
-    args = Kv4Attention(arrays, q.data_ptr(), page_table.data_ptr(), lengths.data_ptr(), offsets, y.data_ptr(),
-                        *_ws_args(workspace), T, B, max_pages, qr, qh, _fp_code(q, "q"), Hq, 1 if causal else 0,
-                        min(window, _I32 - 1), D ** -0.5 if softmax_scale is None else softmax_scale)
-    st = lib().cider_kv4_attention(ctypes.byref(args), _raw_stream(stream, dev))
+        _need_on(dev, y, t, shape, "y")
+    space, size = 0, _attention_workspace_size(T, B, Hq, arrays[6], D, max_pages * arrays[5])
+    if workspace is not None:
+        _, size = _ws_args(workspace)
+        if workspace.get_device() != dev:
+            raise ValueError(f"workspace must be on the current device {dev}, not {workspace.get_device()}")
+    elif size:
+        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+    if workspace is not None:
+        space = workspace.data_ptr()
+    args = _pack_attention(*arrays, q.data_ptr(), page_table.data_ptr(), lengths.data_ptr(), offsets, y.data_ptr(), space, size,
+                           T, B, max_pages, qr, qh, _fp_code(q, "q"), Hq, 1 if causal else 0, min(window, _I32 - 1),
+                           D ** -0.5 if softmax_scale is None else softmax_scale)
+    st = lib().cider_kv4_attention(args, _raw_stream(stream, dev))
     if st:
         _check("cider_kv4_attention", st)
     return y
