@@ -823,7 +823,7 @@ static bool kv4_attention_sizes_ok(int64_t T, int64_t B, int32_t q_heads, int32_
       kv_heads > CIDER_KV4_MAX_HEADS || q_heads < 1 || q_heads > CIDER_KV4_MAX_Q_HEADS || q_heads % kv_heads)
     return false;
   if (head_dim != 64 && head_dim != 128 && head_dim != 256) return false;
-  return T == 0 || (T * q_heads < kLimit && cider::kv4_attention_fits(T, B, q_heads, kv_heads, capacity));
+  return T == 0 || (T * q_heads < kLimit && cider::kv4_attention_fits(T, B, q_heads, kv_heads, head_dim, capacity));
 }
 
 int64_t cider_kv4_attention_workspace_size(int64_t T, int64_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim,

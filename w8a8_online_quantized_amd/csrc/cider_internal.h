@@ -190,7 +190,7 @@ struct Kv4AttentionArgs {
   float softmax_scale;
 };
 // Sizes whose grid of workgroups fits a launch.
-bool kv4_attention_fits(int64_t T, int64_t B, int q_heads, int kv_heads, int64_t capacity);
+bool kv4_attention_fits(int64_t T, int64_t B, int q_heads, int kv_heads, int head_dim, int64_t capacity);
 int64_t kv4_attention_workspace_bytes(int64_t T, int64_t B, int q_heads, int kv_heads, int head_dim, int64_t capacity);
 hipError_t launch_kv4_attention(const Kv4AttentionArgs& args, bool bf16, hipStream_t stream);
 

@@ -8,31 +8,31 @@
 //
 // A "row" is one (query token, query head); the rows of one key/value head's
 // query heads are packed token by token into tiles of 16, so that a group of
-// heads shares each read of the cache. One wave holds NQ such tiles and walks
-// the tokens 32 at a time with both operands straight from global memory to
-// registers: the codes are an eighth of a 16-bit cache's bytes, so nothing is
-// gained by staging them. Per 32 tokens:
+// heads shares each read of the cache. Tokens are taken 32 at a time:
 //   S^T = K Q^T  v_mfma_f32_16x16x32, tokens as rows. A nibble n becomes an operand
 //        by a mask and an or: the fp16 pattern 0x5400 | n << 4 is 64 + n, the bf16
 //        pattern 0x4300 | n is 128 + n. The sums start at -72 * sum(q) (-136 *
 //        sum(q)), so taking n to n - 8 costs nothing, and s_k scales the finished
 //        fp32 sums. (fp16 denormals, n * 2^-24, would need no or, but the matrix
 //        core aligns products by their exponent fields: sums of them lose ten bits.)
-//   p = 2^(S - m): four tokens of one query per lane and sub-tile, which is the
+//   p = 2^(S - m): four tokens of one query per lane and 16 tokens, which is the
 //        layout in which the next product reads them. p * s_v is rounded to fp16
 //        (both types: 2^-11 relative, where bf16 would leave 2^-8); s_v is taken
 //        relative to a power of two that follows the largest one seen, so that
 //        scales of any size fit.
-//   O^T += V^T P^T  v_mfma_f32_16x16x32_f16, 16 dimensions as rows: a lane reads its
-//        sixteenth of eight tokens' rows, and two v_perm and a few masks turn the
-//        words into operands 64 + n. A product with a constant 72 sums what is too much.
+//   O^T += V^T P^T  v_mfma_f32_16x16x32_f16, 16 dimensions as rows: operand j is nibble
+//        j of a lane's sixteenth of eight tokens' rows, as 64 + n. A product with a
+//        constant 72 sums what is too much.
 // m is raised only when a score passes it by 2^8 (the accumulators are rescaled
 // then), so most steps exchange nothing between lanes.
 //
-// SPLIT: the four waves of a workgroup share one tile of rows and take the
-// tokens in turn; otherwise each wave has rows of its own. Either way the
-// tokens are also split over workgroups when there are few rows; their partial
-// results are joined by a second launch.
+// Two kernels. kv4_tokens is for few rows (a decode step): the four waves of a
+// workgroup share a tile of 16 rows and take the tokens in turn, codes from
+// global memory straight to registers; what bounds it is the stream of the
+// codes. kv4_rows is for many: each wave has 32 rows, and the workgroup
+// unpacks a stage of tokens once, into LDS, in the operands' own order. In both
+// the tokens are also split over workgroups when there are few tiles; their
+// partial results are joined by a second launch.
 #include "cider_internal.h"
 #include "cider_quant_rule.h"
 #include "cider_rows.h"
@@ -44,12 +44,15 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int kTokens = 32;            // per step of a wave
+constexpr int kTokens = 32;            // of one step of products
+// Tiles of 16 rows of a wave of kv4_rows: what 256 registers hold without spills.
+constexpr int row_tiles(int D, int G) { return D == 256 || D / G == 32 ? 1 : 2; }
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLeast = -3.402823466e38f;
 constexpr float kRaise = 8.0f;         // log2: p stays below 2^8
 
 typedef float f4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u2 __attribute__((ext_vector_type(2)));
 
 template <bool BF>
 __device__ __forceinline__ f4 mfma_qk(u4 a, u4 b, f4 c) {
@@ -63,6 +66,9 @@ __device__ __forceinline__ f4 mfma_pv(u4 a, u4 b, f4 c) {
 }
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ float uniform(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, v)));
+}
 
 typedef __attribute__((address_space(1))) const uint8_t gbyte;
 
@@ -71,10 +77,19 @@ __device__ __forceinline__ T gload(gbyte* p) { return *(__attribute__((address_s
 
 // ---- which rows and tokens a workgroup has ------------------------------------
 
+// The launch: how rows are tiled and tokens split (the same in the join).
+struct Plan {
+  int rows;            // of a workgroup's tile
+  int unit;            // tokens of one step of a workgroup's loop
+  int parts, least;    // most workgroups per tile, fewest steps of one
+  int64_t slots;       // tiles over all sequences, at most
+  int64_t tiles_per;   // without query_offsets: tiles of each sequence
+};
+
 // Token range of one tile of rows, and how many workgroups share it.
 struct Share {
   int begin, end;      // tokens [begin, end) that any of its rows sees
-  int steps;           // of kTokens, from begin rounded down
+  int steps;           // of plan.unit, from begin rounded down
   int per, parts;      // steps of one part
 };
 
@@ -82,12 +97,6 @@ struct Sequence {
   int64_t q0;          // first query row
   int n, length;       // queries, tokens in the cache
 };
-
-__device__ __forceinline__ int clamp_length(const Kv4AttentionArgs& a, int64_t b) {
-  const int64_t cap = a.max_pages << a.cache.page_shift;
-  const int len = a.lengths[b];
-  return len < 0 ? 0 : len > cap ? (int)cap : len;
-}
 
 __device__ __forceinline__ Sequence sequence(const Kv4AttentionArgs& a, int64_t b) {
   Sequence s;
@@ -101,31 +110,102 @@ __device__ __forceinline__ Sequence sequence(const Kv4AttentionArgs& a, int64_t 
     s.n = (int)(a.T / a.B);
     s.q0 = b * s.n;
   }
-  s.length = clamp_length(a, b);
+  const int64_t cap = a.max_pages << a.cache.page_shift;
+  const int len = a.lengths[b];
+  s.length = len < 0 ? 0 : len > cap ? (int)cap : len;
   return s;
 }
 
 // tok_lo, tok_hi: the first and the last query token of the tile.
-__device__ __forceinline__ Share share(const Kv4AttentionArgs& a, const Sequence& s, int tok_lo, int tok_hi, int parts,
-                                       int least) {
+__device__ __forceinline__ Share share(const Kv4AttentionArgs& a, const Plan& plan, const Sequence& s, int tok_lo,
+                                       int tok_hi) {
   Share r;
   const int p_lo = s.length - s.n + tok_lo, p_hi = s.length - s.n + tok_hi;
   r.end = a.causal ? min(s.length, p_hi + 1) : s.length;
   r.begin = a.window ? max(0, p_lo - a.window + 1) : 0;
-  r.steps = r.end > r.begin ? (r.end - (r.begin & ~(kTokens - 1)) + kTokens - 1) / kTokens : 0;
-  r.parts = min(parts, max(1, (r.steps + least - 1) / least));
+  r.steps = r.end > r.begin ? (r.end - (r.begin & ~(plan.unit - 1)) + plan.unit - 1) / plan.unit : 0;
+  r.parts = min(plan.parts, max(1, (r.steps + plan.least - 1) / plan.least));
   r.per = max(1, (r.steps + r.parts - 1) / r.parts);
   r.parts = max(1, (r.steps + r.per - 1) / r.per);
   return r;
 }
 
-// The launch: how rows are tiled and tokens split (the same on both sides).
-struct Plan {
-  int rows;            // of a workgroup's tile
-  int parts, least;    // most workgroups per tile, fewest steps of one
-  int64_t slots;       // tiles over all sequences, at most
-  int64_t tiles_per;   // without query_offsets: tiles of each sequence
+struct Tile {
+  int h, heads;        // key/value head, query heads of each
+  int part;
+  int64_t b;
+  Sequence seq;
+  int rows, row0;      // rows of the sequence and head, the tile's first
+  Share sh;
 };
+
+// The workgroup's tile and part; false where it has none (all threads alike).
+__device__ __forceinline__ bool find_tile(const Kv4AttentionArgs& a, const Plan& plan, int lane, Tile& t) {
+  const int hkv = a.cache.kv_heads;
+  t.heads = a.q_heads / hkv;
+  t.h = blockIdx.x % hkv;
+  const int64_t rest = blockIdx.x / hkv;
+  t.part = (int)(rest % plan.parts);
+  const int64_t slot = plan.slots - 1 - rest / plan.parts;      // late tiles see the most tokens: they go first
+  int tile = 0;
+  if (a.query_offsets) {
+    // tiles before each sequence, 64 sequences at a time; every wave alike
+    int64_t before = 0;
+    bool found = false;
+    for (int64_t b0 = 0; b0 < a.B && !found; b0 += 64) {
+      int count = 0;
+      if (b0 + lane < a.B) count = (int)(((int64_t)sequence(a, b0 + lane).n * t.heads + plan.rows - 1) / plan.rows);
+      int sum = count;
+#pragma unroll
+      for (int off = 1; off < 64; off <<= 1) {
+        const int up = __shfl_up(sum, off);
+        if (lane >= off) sum += up;
+      }
+      const uint64_t hit = __ballot(before + sum > slot);
+      if (hit) {
+        const int first = __builtin_ctzll(hit);
+        t.b = uniform((int)b0 + first);
+        tile = uniform((int)(slot - before) - (__shfl(sum, first) - __shfl(count, first)));
+        found = true;
+      }
+      before += __shfl(sum, 63);
+    }
+    if (!found) return false;
+  } else {
+    t.b = slot / plan.tiles_per;
+    tile = (int)(slot - t.b * plan.tiles_per);
+  }
+  t.seq = sequence(a, t.b);
+  t.rows = t.seq.n * t.heads;
+  t.row0 = tile * plan.rows;
+  t.sh = share(a, plan, t.seq, t.row0 / t.heads, (min(t.rows, t.row0 + plan.rows) - 1) / t.heads);
+  return t.part < t.sh.parts;
+}
+
+// Tokens that every row of a wave sees, and that some row sees.
+struct Sight {
+  int all_lo, all_hi, any_lo, any_hi;
+};
+__device__ __forceinline__ Sight sight(const Kv4AttentionArgs& a, const Tile& t, int first_row, int n_rows) {
+  const int last = min(first_row + n_rows, t.rows) - 1;
+  const int p0 = t.seq.length - t.seq.n + first_row / t.heads, p1 = t.seq.length - t.seq.n + max(last, 0) / t.heads;
+  Sight s;
+  s.all_hi = a.causal ? min(t.seq.length, p0 + 1) : t.seq.length;
+  s.any_hi = last < first_row ? 0 : a.causal ? min(t.seq.length, p1 + 1) : t.seq.length;
+  s.all_lo = a.window ? max(0, p1 - a.window + 1) : 0;
+  s.any_lo = a.window ? max(0, p0 - a.window + 1) : 0;
+  return s;
+}
+
+// The page of the sub-tile of 16 tokens at t, -1 where there is nothing to read.
+__device__ __forceinline__ int page_at(const Kv4AttentionArgs& a, int64_t b, int t, int end) {
+  int p = -1;
+  if (t < end) {
+    p = a.page_table[b * a.max_pages + (t >> a.cache.page_shift)];
+    if (p < 0 || p >= a.cache.n_pages) p = -1;
+  }
+  return p;
+}
 
 // ---- the operands ---------------------------------------------------------------
 
@@ -145,162 +225,266 @@ __device__ __forceinline__ u4 k_order(u4 q) {
   return u4{__builtin_amdgcn_perm(q.z, q.x, 0x05040100u), __builtin_amdgcn_perm(q.z, q.x, 0x07060302u),
             __builtin_amdgcn_perm(q.w, q.y, 0x05040100u), __builtin_amdgcn_perm(q.w, q.y, 0x07060302u)};
 }
+// Nibble n of the 16-bit halves of four words (tokens 2i, 2i + 1) as an operand 64 + n.
+__device__ __forceinline__ u4 v_operand(u4 w, int n) {
+  return ((n == 0 ? w << 4 : w >> (4 * n - 4)) & 0x00F000F0u) | 0x54005400u;
+}
 
+// A power of two above v (from 2^-126 to 2^126), and the inverse of such a one.
+__device__ __forceinline__ float power_above(float v) {
+  const uint32_t bits = (__builtin_bit_cast(uint32_t, v) & 0x7F800000u) + 0x00800000u;
+  return __builtin_bit_cast(float, min(bits, 0x7E800000u));
+}
+__device__ __forceinline__ float power_inverse(float v) {
+  return __builtin_bit_cast(float, 0x7F000000u - __builtin_bit_cast(uint32_t, v));
+}
+
+// ---- the rows of a wave -----------------------------------------------------------
+
+template <int D, int G, int NQ>
+struct Rows {
+  static constexpr int kTiles = D / 16, kPer = kTiles / G, kSteps = D / 32;
+  u4 q[NQ][kSteps];          // operands of the scores
+  float q_off[NQ][G];        // what the offset of K's operands adds, negated
+  f4 o[NQ][kTiles];          // sums of (p s_v / ref) (64 + n): dimension sixteenths 4 kb + e of query l16
+  f4 z[NQ][G];               // 72 times the sums of p s_v / ref
+  float m[NQ], l[NQ];        // log2 maximum (in steps of kRaise), this lane's part of the sum of p
+  float over[NQ];            // how far a score may pass m: kRaise, or kLeast while no token was seen
+  float ref[G];              // the power of two by which s_v is divided
+  int64_t to[NQ];            // row of y, -1 behind the last one
+  int lo[NQ], hi[NQ];        // tokens that the row sees
+
+  template <bool BF>
+  __device__ __forceinline__ void begin(const Kv4AttentionArgs& a, const Tile& t, int first_row, int lane) {
+    const int l16 = lane & 15, kb = lane >> 4;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      const int r = first_row + 16 * i + l16;
+      const bool real = r < t.rows;
+      const int rr = real ? r : t.rows - 1;
+      const int tok = rr / t.heads, head = t.h * t.heads + rr - tok * t.heads;
+      const int pos = t.seq.length - t.seq.n + tok;
+      to[i] = real ? (t.seq.q0 + tok) * a.q_heads + head : -1;
+      hi[i] = a.causal ? min(t.seq.length, pos + 1) : t.seq.length;
+      lo[i] = a.window ? max(0, pos - a.window + 1) : 0;
+      const uint16_t* src = static_cast<const uint16_t*>(a.q) + (t.seq.q0 + tok) * a.q_row_stride + head * a.q_head_stride;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int st = 0; st < kSteps / G; ++st) {
+          const u4 w = load16(src + g * (D / G) + kb * (D / G / 4) + st * 8, 0);
+          float v[8];
+          unpack8<BF>(w, v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sum += v[e];
+          q[i][g * (kSteps / G) + st] = k_order(w);
+        }
+        sum += __shfl_xor(sum, 16);
+        sum += __shfl_xor(sum, 32);
+        q_off[i][g] = sum * (BF ? -136.0f : -72.0f);
+      }
+      m[i] = l[i] = 0.0f;
+      over[i] = kLeast;
+#pragma unroll
+      for (int j = 0; j < kTiles; ++j) o[i][j] = f4{0, 0, 0, 0};
+#pragma unroll
+      for (int g = 0; g < G; ++g) z[i][g] = f4{0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int g = 0; g < G; ++g) ref[g] = 0x1p-126f;
+  }
+
+  // V's scales of group g are in units of `to_ref` (a power of two) from here on.
+  __device__ __forceinline__ void units(int g, float to_ref) {
+    const float f = ref[g] * power_inverse(to_ref);
+    ref[g] = to_ref;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) o[i][g * kPer + j] *= f;
+      z[i][g] *= f;
+    }
+  }
+
+  // 32 tokens from `token` on. k(s, step), v(j): operands of sub-tile s and of
+  // output tile j; ks(s, g): log2 scales of the scores of tokens 16 s + 4 kb ..,
+  // vs(s, g): scales of V in units of ref. masked: not every row sees every token;
+  // there(s): sub-tile s may be read at all.
+  template <bool BF, class K, class V, class KS, class VS, class There>
+  __device__ __forceinline__ void step(int token, int kb, bool masked, K k, V v, KS ks, VS vs, There there) {
+    float x[NQ][8];                      // scores less m
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        f4 acc[NQ];
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) acc[i] = f4{q_off[i][g], q_off[i][g], q_off[i][g], q_off[i][g]};
+#pragma unroll
+        for (int st = 0; st < kSteps / G; ++st) {
+          const u4 op = k(s, g * (kSteps / G) + st);
+#pragma unroll
+          for (int i = 0; i < NQ; ++i) acc[i] = mfma_qk<BF>(op, q[i][g * (kSteps / G) + st], acc[i]);
+        }
+        const f4 scale = ks(s, g);
+#pragma unroll
+        for (int i = 0; i < NQ; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            x[i][4 * s + e] = __builtin_fmaf(acc[i][e], scale[e], g == 0 ? -m[i] : x[i][4 * s + e]);
+      }
+    }
+    if (masked) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int tok = token + 16 * (e >> 2) + 4 * kb + (e & 3);
+        const bool some = there(e >> 2);
+#pragma unroll
+        for (int i = 0; i < NQ; ++i)
+          x[i][e] = some && tok >= lo[i] && tok < hi[i] ? x[i][e] : -__builtin_inff();
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    float most[NQ];
+    bool raise = false;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      most[i] = x[i][0];
+#pragma unroll
+      for (int e = 1; e < 8; ++e) most[i] = __builtin_fmaxf(most[i], x[i][e]);
+      raise |= most[i] > over[i];
+    }
+    if (__any(raise)) {
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
+        most[i] = __builtin_fmaxf(most[i], __shfl_xor(most[i], 16));
+        most[i] = __builtin_fmaxf(most[i], __shfl_xor(most[i], 32));
+        const bool fresh = over[i] != kRaise, seen = most[i] > kLeast;
+        // up, or down too when these are the row's first tokens
+        const float by = !seen ? 0.0f : fresh ? most[i] : __builtin_fmaxf(most[i], 0.0f);
+        const float f = fresh ? 1.0f : __builtin_amdgcn_exp2f(-by);
+        m[i] += by;
+        if (seen) over[i] = kRaise;
+        l[i] *= f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[i][e] -= by;
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j) o[i][j] *= f;
+#pragma unroll
+        for (int g = 0; g < G; ++g) z[i][g] *= f;
+      }
+    }
+    u4 p16[NQ][G];
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      float p[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        p[e] = __builtin_amdgcn_exp2f(x[i][e]);
+        l[i] += p[e];
+      }
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const f4 v0 = vs(0, g), v1 = vs(1, g);
+        f8 w;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = p[e] * (e < 4 ? v0[e & 3] : v1[e & 3]);
+        if (masked) {                    // a hidden token's scale may be anything
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[e] = x[i][e] == -__builtin_inff() ? 0.0f : w[e];
+        }
+        p16[i][g] = __builtin_bit_cast(u4, __builtin_convertvector(w, h8));
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    const u4 seventy_two = u4{0x54805480u, 0x54805480u, 0x54805480u, 0x54805480u};
+#pragma unroll
+    for (int i = 0; i < NQ; ++i)
+#pragma unroll
+      for (int g = 0; g < G; ++g) z[i][g] = mfma_pv(seventy_two, p16[i][g], z[i][g]);
+#pragma unroll
+    for (int j = 0; j < kTiles; ++j) {
+      const u4 op = v(j);
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) o[i][j] = mfma_pv(op, p16[i][j / kPer], o[i][j]);
+    }
+  }
+
+  // o becomes the rows' averages; m and l those of the whole row.
+  __device__ __forceinline__ void finish() {
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      l[i] += __shfl_xor(l[i], 16);
+      l[i] += __shfl_xor(l[i], 32);
+      if (over[i] != kRaise) m[i] = kLeast;
+      const float inv = l[i] == 0.0f ? 0.0f : 1.0f / l[i];
+#pragma unroll
+      for (int j = 0; j < kTiles; ++j) o[i][j] = (o[i][j] - z[i][j / kPer]) * (ref[j / kPer] * inv);
+    }
+  }
+
+  // Dimension of sixteenth u (of 16) and code j of it.
+  static __device__ __forceinline__ int dim(int u, int j) { return (j / kPer) * (D / G) + u * kPer + j % kPer; }
+};
+
+// Partial results: fp32 averages [parts][T * q_heads][D], then (m, l) of each.
+__device__ __forceinline__ float* part_row(const Kv4AttentionArgs& a, int part, int64_t row, int D) {
+  return a.workspace + (part * a.T * a.q_heads + row) * D;
+}
+__device__ __forceinline__ float2* part_ml(const Kv4AttentionArgs& a, const Plan& plan, int part, int64_t row, int D) {
+  return reinterpret_cast<float2*>(a.workspace + plan.parts * a.T * a.q_heads * D) + part * a.T * a.q_heads + row;
+}
+
+// ---- few rows -------------------------------------------------------------------
+
+// One step's 32 tokens as loaded: a lane has the codes of its K row (l16) and of
+// its sixteenth of eight V rows, and one token's scale of K (lanes 0 .. 31) or V.
 template <int D, int G>
-struct Raw {                            // 32 tokens as loaded
+struct Raw {
   static constexpr int kVW = D / 128 ? D / 128 : 1;   // words of a sixteenth of a V row
   uint32_t k[2][D / 32];
   uint32_t v[8][kVW];
-  f4 ks[2][G], vs[2][G];
+  float s[G];
 };
 
-template <int D, int G, bool BF, int NQ, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, 2) kv4_attention(Kv4AttentionArgs a, Plan plan) {
-  constexpr int kTiles = D / 16;        // output tiles of 16 dimensions; also the codes of a sixteenth
-  constexpr int kPer = kTiles / G;      // of one group
-  constexpr int kSteps = D / 32;        // products of one score
-  constexpr int kRowsW = 16 * NQ;       // rows of a wave
-  constexpr int kPitch = D + 4;
-  __shared__ float shared_o[SPLIT ? kWaves * 16 * NQ * kPitch : 1];
-  __shared__ float shared_m[SPLIT ? kWaves * 16 * NQ : 1], shared_l[SPLIT ? kWaves * 16 * NQ : 1];
-
-  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const int l16 = lane & 15, kb = lane >> 4;
-  const int hkv = a.cache.kv_heads, heads = a.q_heads / hkv;
-
-  // ---- the workgroup's tile
-  const int h = blockIdx.x % hkv;
-  const int64_t rest = blockIdx.x / hkv;
-  const int part = (int)(rest % plan.parts);
-  const int64_t slot = plan.slots - 1 - rest / plan.parts;      // late tiles see the most tokens: they go first
-  int64_t b = 0;
-  int tile = 0;
-  if (a.query_offsets) {
-    // tiles before each sequence, 64 sequences at a time; every wave alike
-    int64_t before = 0;
-    bool found = false;
-    for (int64_t b0 = 0; b0 < a.B && !found; b0 += 64) {
-      int count = 0;
-      if (b0 + lane < a.B) count = (int)(((int64_t)sequence(a, b0 + lane).n * heads + plan.rows - 1) / plan.rows);
-      int sum = count;
-#pragma unroll
-      for (int off = 1; off < 64; off <<= 1) {
-        const int up = __shfl_up(sum, off);
-        if (lane >= off) sum += up;
-      }
-      const uint64_t hit = __ballot(before + sum > slot);
-      if (hit) {
-        const int first = __builtin_ctzll(hit);
-        b = b0 + first;
-        tile = (int)(slot - before) - (__shfl(sum, first) - __shfl(count, first));
-        found = true;
-      }
-      before += __shfl(sum, 63);
-    }
-    if (!found) return;
-    b = uniform((int)b);
-    tile = uniform(tile);
-  } else {
-    b = slot / plan.tiles_per;
-    tile = (int)(slot - b * plan.tiles_per);
-  }
-  const Sequence seq = sequence(a, b);
-  const int rows = seq.n * heads;       // of this sequence and key/value head
-  const int row0 = tile * plan.rows;
-  const Share sh = share(a, seq, row0 / heads, (min(rows, row0 + plan.rows) - 1) / heads, plan.parts, plan.least);
-  if (part >= sh.parts) return;
-  const int step_end = min(sh.steps, (part + 1) * sh.per);
-  const int first_token = sh.begin & ~(kTokens - 1);
-
-  // ---- the wave's rows
-  const int wrow0 = row0 + (SPLIT ? 0 : wave * kRowsW);
-  int64_t q_row[NQ];                    // row of y (and of the partial results), -1 behind the last one
-  int see_lo[NQ], see_hi[NQ];
-  u4 qf[NQ][kSteps];
-  f4 q_off[NQ][G];
-#pragma unroll
-  for (int i = 0; i < NQ; ++i) {
-    const int r = wrow0 + 16 * i + l16;
-    const bool real = r < rows;
-    const int rr = real ? r : rows - 1;
-    const int tok = rr / heads, head = h * heads + rr - tok * heads;
-    const int pos = seq.length - seq.n + tok;
-    q_row[i] = real ? (seq.q0 + tok) * a.q_heads + head : -1;
-    see_hi[i] = a.causal ? min(seq.length, pos + 1) : seq.length;
-    see_lo[i] = a.window ? max(0, pos - a.window + 1) : 0;
-    const uint16_t* q = static_cast<const uint16_t*>(a.q) + (seq.q0 + tok) * a.q_row_stride + head * a.q_head_stride;
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      float sum = 0.0f;
-#pragma unroll
-      for (int st = 0; st < kSteps / G; ++st) {
-        const u4 w = load16(q + g * (D / G) + kb * (D / G / 4) + st * 8, 0);
-        float t[8];
-        unpack8<BF>(w, t);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum += t[e];
-        qf[i][g * (kSteps / G) + st] = k_order(w);
-      }
-      sum += __shfl_xor(sum, 16);
-      sum += __shfl_xor(sum, 32);
-      const float off = sum * (BF ? -136.0f : -72.0f);
-      q_off[i][g] = f4{off, off, off, off};
-    }
-  }
-  // tokens that every row of the wave sees, and that some row sees (uniform)
-  int all_lo = 0, all_hi = 0, any_hi = 0, any_lo = 0;
-  {
-    const int last = min(wrow0 + kRowsW, rows) - 1;
-    const int p0 = seq.length - seq.n + wrow0 / heads, p1 = seq.length - seq.n + max(last, 0) / heads;
-    all_hi = a.causal ? min(seq.length, p0 + 1) : seq.length;
-    any_hi = a.causal ? min(seq.length, p1 + 1) : seq.length;
-    all_lo = a.window ? max(0, p1 - a.window + 1) : 0;
-    any_lo = a.window ? max(0, p0 - a.window + 1) : 0;
-    if (last < wrow0) any_hi = 0;       // a wave behind the last row
-  }
-
-  f4 o[NQ][kTiles], z[NQ][G];
-  float m[NQ], l[NQ];
-  float ref = 0x1p-126f, inv_ref = 0x1p126f;
-#pragma unroll
-  for (int i = 0; i < NQ; ++i) {
-    m[i] = kLeast;
-    l[i] = 0.0f;
-#pragma unroll
-    for (int j = 0; j < kTiles; ++j) o[i][j] = f4{0, 0, 0, 0};
-#pragma unroll
-    for (int g = 0; g < G; ++g) z[i][g] = f4{0, 0, 0, 0};
-  }
-
-  const float scale = a.softmax_scale * kLog2e;
-  const int32_t* table = a.page_table + b * a.max_pages;
-  const int page_size = a.cache.page_size, page_shift = a.cache.page_shift;
-
-  // The pages of 64 sub-tiles of 16 tokens from the wave's step `first` on (a
-  // lane each, -1 where there is nothing to read), so that the steps' loads wait
-  // for no table entry.
-  constexpr int kStride = SPLIT ? kWaves : 1;
-  auto pages_from = [&](int first) {
-    const int t = first_token + (first + (lane >> 1) * kStride) * kTokens + (lane & 1) * 16;
-    int p = -1;
-    if (t < any_hi) {
-      p = table[t >> page_shift];
-      if (p < 0 || p >= a.cache.n_pages) p = -1;
-    }
-    return p;
+template <int D, int G, bool BF>
+__global__ void __launch_bounds__(kThreads, D == 256 ? 2 : G == 4 ? 2 : 3) kv4_tokens(Kv4AttentionArgs a, Plan plan) {
+  using R = Rows<D, G, 1>;
+  constexpr int kSteps = R::kSteps, kPitch = D + 4;
+  union Shared {
+    struct {
+      float o[kWaves][16][kPitch], m[kWaves][16], l[kWaves][16];
+    } out;
+    float s[kWaves][G][64];              // a step's scales, each wave its own
   };
-  using R = Raw<D, G>;
-  auto load = [&](int t, const int (&pages)[2], R& r) {
+  __shared__ Shared shared;
+  const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
+  const int l16 = lane & 15, kb = lane >> 4;
+  Tile t;
+  if (!find_tile(a, plan, lane, t)) return;
+  R rows;
+  rows.template begin<BF>(a, t, t.row0, lane);
+  const Sight see = sight(a, t, t.row0, 16);
+  const int step_end = min(t.sh.steps, (t.part + 1) * t.sh.per);
+  const int first_token = t.sh.begin & ~(kTokens - 1);
+  const float scale = a.softmax_scale * kLog2e;
+  const int page_size = a.cache.page_size, hkv = a.cache.kv_heads;
+
+  const uint32_t k_lane = l16 * (D / 2) + kb * (D / G / 8), v_lane = 4 * kb * (D / 2) + l16 * (D / 32);
+  auto load = [&](int token, const int (&pages)[2], Raw<D, G>& r) {
+    int64_t ph[2];
+    int at[2];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const bool there = pages[s] >= 0;
-      const int at = there ? (t + 16 * s) & (page_size - 1) : 0;
-      const int64_t ph = (int64_t)(there ? pages[s] : 0) * hkv + h;
-      const int64_t base = (ph * page_size + at) * (D / 2);
-      gbyte* k = (gbyte*)a.cache.k_codes + base + l16 * (D / 2) + kb * (D / G / 8);
+      at[s] = there ? (token + 16 * s) & (page_size - 1) : 0;
+      ph[s] = (int64_t)(there ? pages[s] : 0) * hkv + t.h;
+      const int64_t base = (ph[s] * page_size + at[s]) * (D / 2);
+      gbyte* k = (gbyte*)a.cache.k_codes + base;      // uniform; the lane's part is a 32-bit offset
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        gbyte* kg = k + g * (D / G / 2);
+        gbyte* kg = k + k_lane + g * (D / G / 2);
         constexpr int kW = kSteps / G;
         if constexpr (kW % 4 == 0) {
 #pragma unroll
@@ -310,7 +494,6 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attention(Kv4AttentionArgs a,
             for (int e = 0; e < 4; ++e) r.k[s][g * kW + 4 * i + e] = w[e];
           }
         } else if constexpr (kW == 2) {
-          typedef uint32_t u2 __attribute__((ext_vector_type(2)));
           const u2 w = gload<u2>(kg);
           r.k[s][g * kW] = w.x;
           r.k[s][g * kW + 1] = w.y;
@@ -318,172 +501,68 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attention(Kv4AttentionArgs a,
           r.k[s][g] = gload<uint32_t>(kg);
         }
       }
-      gbyte* v = (gbyte*)a.cache.v_codes + base + 4 * kb * (D / 2) + l16 * (D / 32);
+      gbyte* v = (gbyte*)a.cache.v_codes + base;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        gbyte* vi = v + i * (D / 2);
+        gbyte* vi = v + v_lane + i * (D / 2);
         if constexpr (D == 64) r.v[4 * s + i][0] = gload<uint16_t>(vi);
         else if constexpr (D == 128) r.v[4 * s + i][0] = gload<uint32_t>(vi);
         else {
-          typedef uint32_t u2 __attribute__((ext_vector_type(2)));
           const u2 w = gload<u2>(vi);
           r.v[4 * s + i][0] = w.x;
           r.v[4 * s + i][1] = w.y;
         }
       }
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const int64_t so = ((ph * G + g) * page_size + at + 4 * kb) * 4;
-        r.ks[s][g] = gload<f4>((gbyte*)a.cache.k_scale + so);
-        r.vs[s][g] = gload<f4>((gbyte*)a.cache.v_scale + so);
-      }
     }
+    const bool second = lane & 16;
+    const int64_t so = (second ? ph[1] : ph[0]) * G * page_size + (second ? at[1] : at[0]) + l16;
+    gbyte* from = lane < 32 ? (gbyte*)a.cache.k_scale : (gbyte*)a.cache.v_scale;
+#pragma unroll
+    for (int g = 0; g < G; ++g) r.s[g] = gload<float>(from + (so + g * page_size) * 4);
   };
 
-  auto process = [&](int t, const int (&pages)[2], const R& r) {
-    // scores, in units of log2
-    float x[NQ][8];
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        f4 acc[NQ];
-#pragma unroll
-        for (int i = 0; i < NQ; ++i) acc[i] = q_off[i][g];
-#pragma unroll
-        for (int st = 0; st < kSteps / G; ++st) {
-          const u4 k = k_operand<BF>(r.k[s][g * (kSteps / G) + st]);
-#pragma unroll
-          for (int i = 0; i < NQ; ++i) acc[i] = mfma_qk<BF>(k, qf[i][g * (kSteps / G) + st], acc[i]);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float ks = r.ks[s][g][e] * scale;
-#pragma unroll
-          for (int i = 0; i < NQ; ++i)
-            x[i][4 * s + e] = g == 0 ? acc[i][e] * ks : __builtin_fmaf(acc[i][e], ks, x[i][4 * s + e]);
-        }
-      }
-    }
-    float vs[G][8];
-#pragma unroll
-    for (int g = 0; g < G; ++g)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) vs[g][e] = r.vs[e >> 2][g][e & 3];
-    // tokens that not every row sees
-    const bool masked = t < all_lo || t + kTokens > all_hi || pages[0] < 0 || pages[1] < 0;
+  auto process = [&](int token, const int (&pages)[2], Raw<D, G>& r) {
+    const bool masked = token < see.all_lo || token + kTokens > see.all_hi || pages[0] < 0 || pages[1] < 0;
     if (masked) {
+      // scales that no row may see are nothing
+      const int tok = token + (lane & 31);
+      const bool there0 = pages[0] >= 0, there1 = pages[1] >= 0;
+      const bool some = ((lane & 16) ? there1 : there0) && tok >= see.any_lo && tok < see.any_hi;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int tok = t + 16 * (e >> 2) + 4 * kb + (e & 3);
-        const bool there = pages[e >> 2] >= 0;
-        const bool some = there && tok >= any_lo && tok < any_hi;
-#pragma unroll
-        for (int g = 0; g < G; ++g) vs[g][e] = some ? vs[g][e] : 0.0f;
-#pragma unroll
-        for (int i = 0; i < NQ; ++i)
-          x[i][e] = there && tok >= see_lo[i] && tok < see_hi[i] ? x[i][e] : -__builtin_inff();
-      }
-    }
-    // a larger scale of V than all before: the accumulators are in units of ref
-    float top = 0.0f;
-#pragma unroll
-    for (int g = 0; g < G; ++g)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) top = __builtin_fmaxf(top, __builtin_fabsf(vs[g][e]));
-    if (__any(top > ref)) {
-      for (int off = 32; off >= 1; off >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, off));
-      uint32_t bits = (__builtin_bit_cast(uint32_t, top) & 0x7F800000u) + 0x00800000u;   // the next power of two
-      bits = min(bits, 0x7E800000u);
-      const float to = __builtin_bit_cast(float, bits);
-      inv_ref = __builtin_bit_cast(float, 0x7F000000u - bits);
-      const float f = ref * inv_ref;
-      ref = to;
-#pragma unroll
-      for (int i = 0; i < NQ; ++i) {
-#pragma unroll
-        for (int j = 0; j < kTiles; ++j) o[i][j] *= f;
-#pragma unroll
-        for (int g = 0; g < G; ++g) z[i][g] *= f;
-      }
+      for (int g = 0; g < G; ++g) r.s[g] = some ? r.s[g] : 0.0f;
     }
 #pragma unroll
-    for (int g = 0; g < G; ++g)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) vs[g][e] *= inv_ref;
-
-    u4 pf[NQ][G];
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      float most = x[i][0];
-#pragma unroll
-      for (int e = 1; e < 8; ++e) most = __builtin_fmaxf(most, x[i][e]);
-      if (__any(most > m[i] + kRaise)) {
-        most = __builtin_fmaxf(most, __shfl_xor(most, 16));
-        most = __builtin_fmaxf(most, __shfl_xor(most, 32));
-        const float to = __builtin_fmaxf(m[i], most);
-        const float f = __builtin_amdgcn_exp2f(m[i] - to);
-        m[i] = to;
-        l[i] *= f;
-#pragma unroll
-        for (int j = 0; j < kTiles; ++j) o[i][j] *= f;
-#pragma unroll
-        for (int g = 0; g < G; ++g) z[i][g] *= f;
+    for (int g = 0; g < G; ++g) {
+      const float v = lane < 32 ? 0.0f : __builtin_fabsf(r.s[g]);
+      if (__any(v > rows.ref[g])) {
+        float top = v;
+        for (int off = 16; off >= 1; off >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, off));
+        rows.units(g, power_above(__shfl(top, 32)));
       }
-      float p[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        p[e] = __builtin_amdgcn_exp2f(x[i][e] - m[i]);
-        l[i] += p[e];
-      }
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        f8 w;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = p[e] * vs[g][e];
-        if (masked) {                   // a hidden token's scale may be anything
-#pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] = x[i][e] == -__builtin_inff() ? 0.0f : w[e];
-        }
-        pf[i][g] = __builtin_bit_cast(u4, __builtin_convertvector(w, h8));
-      }
+      shared.s[wave][g][lane] = r.s[g] * (lane < 32 ? scale : power_inverse(rows.ref[g]));
     }
-    // O^T += V^T P^T
-    const u4 seventy_two = u4{0x54805480u, 0x54805480u, 0x54805480u, 0x54805480u};
+    auto k = [&](int s, int st) { return k_operand<BF>(r.k[s][st]); };
+    u4 w[D / 64];
 #pragma unroll
-    for (int i = 0; i < NQ; ++i)
+    for (int c = 0; c < D / 64; ++c)
 #pragma unroll
-      for (int g = 0; g < G; ++g) z[i][g] = mfma_pv(seventy_two, pf[i][g], z[i][g]);
-    constexpr int kHalves = D == 64 ? 1 : D / 64;   // 16-bit columns of a sixteenth: 4 codes each
-#pragma unroll
-    for (int c = 0; c < kHalves; ++c) {
-      u4 w;
-#pragma unroll
-      for (int pr = 0; pr < 4; ++pr) {
-        const uint32_t lo = r.v[2 * pr][c / 2], hi = r.v[2 * pr + 1][c / 2];
-        w[pr] = __builtin_amdgcn_perm(hi, lo, c % 2 ? 0x07060302u : 0x05040100u);
-      }
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const int j = 4 * c + n;
-        const u4 v = ((n == 0 ? w << 4 : w >> (4 * n - 4)) & 0x00F000F0u) | 0x54005400u;
-#pragma unroll
-        for (int i = 0; i < NQ; ++i) o[i][j] = mfma_pv(v, pf[i][j / kPer], o[i][j]);
-      }
-    }
+      for (int pr = 0; pr < 4; ++pr)
+        w[c][pr] = __builtin_amdgcn_perm(r.v[2 * pr + 1][c / 2], r.v[2 * pr][c / 2], c % 2 ? 0x07060302u : 0x05040100u);
+    auto v = [&](int j) { return v_operand(w[j / 4], j % 4); };
+    auto ks = [&](int s, int g) { return *reinterpret_cast<const f4*>(&shared.s[wave][g][16 * s + 4 * kb]); };
+    auto vs = [&](int s, int g) { return *reinterpret_cast<const f4*>(&shared.s[wave][g][32 + 16 * s + 4 * kb]); };
+    auto there = [&](int s) { return s ? pages[1] >= 0 : pages[0] >= 0; };
+    rows.template step<BF>(token, kb, masked, k, v, ks, vs, there);
   };
 
-  // ---- the tokens, the next step's codes on their way during each step
+  // the waves take the steps in turn, the next one's codes on their way during each
   {
-    int step = part * sh.per + (SPLIT ? wave : 0);
-    int stop = step_end;
-    if constexpr (!SPLIT) {
-      // a wave's own rows may see less than the workgroup's
-      stop = min(stop, (any_hi - first_token + kTokens - 1) / kTokens);
-      step = max(step, (any_lo - first_token) / kTokens);
-    }
-    auto token = [&](int s) { return first_token + s * kTokens; };
-    if (step < stop) {
+    int step = t.part * t.sh.per + wave;
+    // the pages of 32 steps, a lane each, so that no step waits for a table entry
+    auto pages_from = [&](int first) {
+      return page_at(a, t.b, first_token + (first + (lane >> 1) * kWaves) * kTokens + (lane & 1) * 16, see.any_hi);
+    };
+    if (step < step_end) {
       int ids = pages_from(step), at = 0;         // `at`: the sub-tile of ids that comes next
       auto take = [&](int (&p)[2]) {
         p[0] = __builtin_amdgcn_readlane(ids, at);
@@ -491,19 +570,19 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attention(Kv4AttentionArgs a,
         at += 2;
       };
       int pages[2], next[2];
-      R cur, nxt;
+      Raw<D, G> cur, nxt;
       take(pages);
-      load(token(step), pages, cur);
-      for (; step < stop; step += kStride) {
-        if (step + kStride < stop) {
+      load(first_token + step * kTokens, pages, cur);
+      for (; step < step_end; step += kWaves) {
+        if (step + kWaves < step_end) {
           if (at == 64) {
-            ids = pages_from(step + kStride);
+            ids = pages_from(step + kWaves);
             at = 0;
           }
           take(next);
-          load(token(step + kStride), next, nxt);
+          load(first_token + (step + kWaves) * kTokens, next, nxt);
         }
-        process(token(step), pages, cur);
+        process(first_token + step * kTokens, pages, cur);
         cur = nxt;
         pages[0] = next[0];
         pages[1] = next[1];
@@ -511,117 +590,267 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attention(Kv4AttentionArgs a,
     }
   }
 
-  // ---- finished rows: a lane holds query l16, dimensions of sixteenths 4 kb .. 4 kb + 3
-  const bool whole = sh.parts == 1;
-  const int64_t all_rows = a.T * a.q_heads;
-#pragma unroll
-  for (int i = 0; i < NQ; ++i) {
-    l[i] += __shfl_xor(l[i], 16);
-    l[i] += __shfl_xor(l[i], 32);
-    const float inv = l[i] == 0.0f ? 0.0f : ref / l[i];
-#pragma unroll
-    for (int j = 0; j < kTiles; ++j) o[i][j] = (o[i][j] - z[i][j / kPer]) * inv;
+  // the waves' parts of each row, joined
+  rows.finish();
+  __syncthreads();                       // every wave is done with its scales
+  if (kb == 0) {
+    shared.out.m[wave][l16] = rows.m[0];
+    shared.out.l[wave][l16] = rows.l[0];
   }
-  auto dim_of = [&](int unit, int j) { return (j / kPer) * (D / G) + unit * kPer + j % kPer; };
-  if constexpr (SPLIT) {
 #pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      const int r = wave * kRowsW + 16 * i + l16;
-      if (kb == 0) {
-        shared_m[r] = m[i];
-        shared_l[r] = l[i];
-      }
+  for (int e = 0; e < 4; ++e)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
+    for (int j = 0; j < R::kTiles; ++j) shared.out.o[wave][l16][R::dim(4 * kb + e, j)] = rows.o[0][j][e];
+  __syncthreads();
+  constexpr int kChunks = D / 8;
+  const int n_rows = min(16, t.rows - t.row0);
+  for (int item = threadIdx.x; item < n_rows * kChunks; item += kThreads) {
+    const int r = item / kChunks, c = item - r * kChunks;
+    float top = kLeast;
 #pragma unroll
-        for (int j = 0; j < kTiles; ++j) shared_o[r * kPitch + dim_of(4 * kb + e, j)] = o[i][j][e];
-    }
-    __syncthreads();
-    constexpr int kChunks = D / 8;
-    const int n_rows = min(kRowsW, rows - row0);
-    for (int item = threadIdx.x; item < n_rows * kChunks; item += kThreads) {
-      const int r = item / kChunks, c = item - r * kChunks;
-      float top = shared_m[r];
+    for (int w = 0; w < kWaves; ++w) top = __builtin_fmaxf(top, shared.out.m[w][r]);
+    float sum = 0.0f, out[8];
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) top = __builtin_fmaxf(top, shared_m[w * kRowsW + r]);
-      float sum = 0.0f, out[8];
+    for (int e = 0; e < 8; ++e) out[e] = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) out[e] = 0.0f;
+    for (int w = 0; w < kWaves; ++w) {
+      const float f = __builtin_amdgcn_exp2f(shared.out.m[w][r] - top) * shared.out.l[w][r];
+      sum += f;
+      if (f != 0.0f) {
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        const float f = __builtin_amdgcn_exp2f(shared_m[w * kRowsW + r] - top) * shared_l[w * kRowsW + r];
-        sum += f;
-        if (f != 0.0f) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            out[e] = __builtin_fmaf(f, shared_o[(w * kRowsW + r) * kPitch + 8 * c + e], out[e]);
-        }
-      }
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) out[e] *= inv;
-      const int tok = (row0 + r) / heads;
-      const int64_t to = (seq.q0 + tok) * a.q_heads + h * heads + (row0 + r) - tok * heads;
-      if (whole) {
-        store16(static_cast<uint16_t*>(a.y) + to * D, c, pack8<BF>(out));
-      } else {
-        float* po = a.workspace + (part * all_rows + to) * D + 8 * c;
-        *reinterpret_cast<f4*>(po) = f4{out[0], out[1], out[2], out[3]};
-        *reinterpret_cast<f4*>(po + 4) = f4{out[4], out[5], out[6], out[7]};
-        if (c == 0) {
-          float* ml = a.workspace + plan.parts * all_rows * D + (part * all_rows + to) * 2;
-          ml[0] = top;
-          ml[1] = sum;
-        }
+        for (int e = 0; e < 8; ++e) out[e] = __builtin_fmaf(f, shared.out.o[w][r][8 * c + e], out[e]);
       }
     }
-  } else {
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      if (q_row[i] < 0) continue;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int unit = 4 * kb + e;
-        if (whole) {
-          uint16_t* y = static_cast<uint16_t*>(a.y) + q_row[i] * D;
-#pragma unroll
-          for (int g = 0; g < G; ++g) {
-            uint16_t* to = y + dim_of(unit, g * kPer);
-            if constexpr (kPer % 8 == 0) {
-#pragma unroll
-              for (int q = 0; q < kPer / 8; ++q) {
-                float t[8];
-#pragma unroll
-                for (int n = 0; n < 8; ++n) t[n] = o[i][g * kPer + 8 * q + n][e];
-                store16(to, q, pack8<BF>(t));
-              }
-            } else {
-#pragma unroll
-              for (int n = 0; n < kPer; n += 2) {
-                const uint32_t two = round16<BF>(o[i][g * kPer + n][e]) | (uint32_t)round16<BF>(o[i][g * kPer + n + 1][e]) << 16;
-                *reinterpret_cast<uint32_t*>(to + n) = two;
-              }
-            }
-          }
-        } else {
-          float* po = a.workspace + (part * all_rows + q_row[i]) * D;
-#pragma unroll
-          for (int g = 0; g < G; ++g)
-#pragma unroll
-            for (int n = 0; n < kPer; n += 2) {
-              float2 two = make_float2(o[i][g * kPer + n][e], o[i][g * kPer + n + 1][e]);
-              *reinterpret_cast<float2*>(po + dim_of(unit, g * kPer + n)) = two;
-            }
-        }
-      }
-      if (!whole && kb == 0) {
-        float* ml = a.workspace + plan.parts * all_rows * D + (part * all_rows + q_row[i]) * 2;
-        ml[0] = m[i];
-        ml[1] = l[i];
-      }
+    for (int e = 0; e < 8; ++e) out[e] *= inv;
+    const int tok = (t.row0 + r) / t.heads;
+    const int64_t to = (t.seq.q0 + tok) * a.q_heads + t.h * t.heads + (t.row0 + r) - tok * t.heads;
+    if (t.sh.parts == 1) {
+      store16(static_cast<uint16_t*>(a.y) + to * D, c, pack8<BF>(out));
+    } else {
+      float* po = part_row(a, t.part, to, D) + 8 * c;
+      *reinterpret_cast<f4*>(po) = f4{out[0], out[1], out[2], out[3]};
+      *reinterpret_cast<f4*>(po + 4) = f4{out[4], out[5], out[6], out[7]};
+      if (c == 0) *part_ml(a, plan, t.part, to, D) = make_float2(top, sum);
     }
   }
 }
+
+// ---- many rows ------------------------------------------------------------------
+
+// Tokens of a stage of kv4_rows: two stages of operands fit the LDS of one of two
+// workgroups of a CU.
+constexpr int stage_tokens(int D) { return D == 256 ? 32 : 64; }
+
+template <int D, int G, bool BF>
+__global__ void __launch_bounds__(kThreads, 2) kv4_rows(Kv4AttentionArgs a, Plan plan) {
+  constexpr int NQ = row_tiles(D, G);
+  using R = Rows<D, G, NQ>;
+  constexpr int S = stage_tokens(D), kSubs = S / 16, kHalves = S / 32;
+  constexpr int kSteps = R::kSteps, kTiles = R::kTiles;
+  // what a wave unpacks: steps of one sub-tile of K, tiles of one half of V
+  constexpr int kKPer = kSteps * kSubs / kWaves, kVPer = kTiles * kHalves / kWaves;
+  constexpr int kArrays = 2 * G;         // of scales: K's groups, then V's
+  __shared__ u4 lds_k[2][kSubs][kSteps][64];
+  __shared__ u4 lds_v[2][kHalves][kTiles][64];
+  __shared__ float lds_s[2][kArrays][S];
+  __shared__ float lds_ref[2][G];
+  const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
+  const int l16 = lane & 15, kb = lane >> 4;
+  Tile t;
+  if (!find_tile(a, plan, lane, t)) return;
+  const int wave_row = t.row0 + wave * 16 * NQ;
+  R rows;
+  rows.template begin<BF>(a, t, wave_row, lane);
+  const Sight see = sight(a, t, wave_row, 16 * NQ);
+  const int stage0 = t.part * t.sh.per, stages = min(t.sh.steps, stage0 + t.sh.per) - stage0;
+  const int first_token = (t.sh.begin & ~(S - 1)) + stage0 * S;
+  const float scale = a.softmax_scale * kLog2e;
+  const int page_size = a.cache.page_size, hkv = a.cache.kv_heads;
+
+  // ---- staging: codes and scales of the next stage in registers
+  const int k_sub = wave % kSubs, k_step = wave / kSubs * kKPer;
+  const int v_half = wave % kHalves, v_tile = wave / kHalves * kVPer;
+  uint32_t raw_k[kKPer], raw_v[8];
+  float raw_s[(kArrays + kWaves - 1) / kWaves];
+  float top_ref[(kArrays + kWaves - 1) / kWaves];      // of the V scales that this wave stages
+#pragma unroll
+  for (float& r : top_ref) r = 0x1p-126f;
+  int ids = 0;                           // pages of 64 sub-tiles, a lane each
+  int have = 0, have_next = 0;           // which sub-tiles of a stage may be read (bits)
+  auto sub_base = [&](int page, int token) {
+    const int at = page >= 0 ? token & (page_size - 1) : 0;
+    return (((int64_t)(page >= 0 ? page : 0) * hkv + t.h) * page_size + at) * (D / 2);
+  };
+  auto load = [&](int stage) {
+    const int token = first_token + stage * S;
+    const int at = stage % (64 / kSubs) * kSubs;
+    if (at == 0) ids = page_at(a, t.b, token + lane * 16, t.sh.end);
+    int pages[kSubs], bits = 0;
+#pragma unroll
+    for (int s = 0; s < kSubs; ++s) {
+      pages[s] = __builtin_amdgcn_readlane(ids, at + s);
+      bits |= (pages[s] >= 0) << s;
+    }
+    have_next = bits;
+    {
+      const int page = __builtin_amdgcn_readlane(ids, at + k_sub);
+      gbyte* k = (gbyte*)a.cache.k_codes + sub_base(page, token + 16 * k_sub) + l16 * (D / 2) + kb * (D / G / 8);
+      constexpr int kW = kSteps / G;     // words of one group in a row's lane
+      if constexpr (kW % 4 == 0 && kKPer % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < kKPer / 4; ++i) {
+          const int st = k_step + 4 * i;
+          const u4 w = gload<u4>(k + st / kW * (D / G / 2) + st % kW * 4);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) raw_k[4 * i + e] = w[e];
+        }
+      } else if constexpr (kW % 2 == 0 && kKPer % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < kKPer / 2; ++i) {
+          const int st = k_step + 2 * i;
+          const u2 w = gload<u2>(k + st / kW * (D / G / 2) + st % kW * 4);
+          raw_k[2 * i] = w.x;
+          raw_k[2 * i + 1] = w.y;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kKPer; ++i) {
+          const int st = k_step + i;
+          raw_k[i] = gload<uint32_t>(k + st / kW * (D / G / 2) + st % kW * 4);
+        }
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {        // 16 bits of a sixteenth, of four tokens' rows
+      const int sub = 2 * v_half + s;
+      const int page = __builtin_amdgcn_readlane(ids, at + sub);
+      gbyte* v = (gbyte*)a.cache.v_codes + sub_base(page, token + 16 * sub) + 4 * kb * (D / 2) + l16 * (D / 32) +
+                 v_tile / 4 * 2;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) raw_v[4 * s + i] = gload<uint16_t>(v + i * (D / 2));
+    }
+    // scales: a token per lane
+    int page = pages[0];
+#pragma unroll
+    for (int s = 1; s < kSubs; ++s) page = kb == s ? pages[s] : page;
+    const int tok = token + (lane & (S - 1));
+    const bool some = page >= 0 && tok >= t.sh.begin && tok < t.sh.end;
+    const int64_t ph = (int64_t)(page >= 0 ? page : 0) * hkv + t.h;
+#pragma unroll
+    for (int i = 0; i < (kArrays + kWaves - 1) / kWaves; ++i) {
+      const int arr = wave + kWaves * i;
+      if (arr >= kArrays) break;
+      const int g = arr < G ? arr : arr - G;
+      gbyte* from = (arr < G ? (gbyte*)a.cache.k_scale : (gbyte*)a.cache.v_scale) +
+                    ((ph * G + g) * page_size + (page >= 0 ? tok & (page_size - 1) : 0)) * 4;
+      const float s = gload<float>(from);
+      raw_s[i] = some ? s : 0.0f;
+    }
+  };
+  auto store = [&](int stage) {
+    const int buf = stage & 1;
+#pragma unroll
+    for (int i = 0; i < kKPer; ++i) lds_k[buf][k_sub][k_step + i][lane] = k_operand<BF>(raw_k[i]);
+    u4 w;
+#pragma unroll
+    for (int pr = 0; pr < 4; ++pr) w[pr] = raw_v[2 * pr] | raw_v[2 * pr + 1] << 16;
+    if constexpr (kVPer == 4) {
+#pragma unroll
+      for (int n = 0; n < 4; ++n) lds_v[buf][v_half][v_tile + n][lane] = v_operand(w, n);
+    } else {                             // half of the four tiles of these 16 bits
+      if (v_tile % 4) w >>= 8;
+#pragma unroll
+      for (int n = 0; n < 2; ++n) lds_v[buf][v_half][v_tile + n][lane] = v_operand(w, n);
+    }
+#pragma unroll
+    for (int i = 0; i < (kArrays + kWaves - 1) / kWaves; ++i) {
+      const int arr = wave + kWaves * i;
+      if (arr >= kArrays) break;
+      float f = scale;
+      if (arr >= G) {
+        float top = __builtin_fabsf(raw_s[i]);
+        if (__any(top > top_ref[i])) {
+          for (int off = 32; off >= 1; off >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, off));
+          top_ref[i] = power_above(top);
+        }
+        f = power_inverse(top_ref[i]);
+        if (lane == 0) lds_ref[buf][arr - G] = top_ref[i];
+      }
+      if (lane < S) lds_s[buf][arr][lane] = raw_s[i] * f;
+    }
+  };
+
+  if (stages > 0) {
+    load(0);
+    store(0);
+  }
+  __syncthreads();
+  for (int stage = 0; stage < stages; ++stage) {
+    have = have_next;
+    if (stage + 1 < stages) load(stage + 1);
+    const int buf = stage & 1, token = first_token + stage * S;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const float to = uniform(lds_ref[buf][g]);
+      if (to != uniform(rows.ref[g])) rows.units(g, to);
+    }
+#pragma unroll
+    for (int half = 0; half < kHalves; ++half) {
+      const int first = token + 32 * half;
+      if (first >= see.any_hi || first + 32 <= see.any_lo) continue;
+      const int bits = have >> (2 * half) & 3;
+      auto k = [&](int s, int st) { return lds_k[buf][2 * half + s][st][lane]; };
+      auto v = [&](int j) { return lds_v[buf][half][j][lane]; };
+      auto ks = [&](int s, int g) { return *reinterpret_cast<const f4*>(&lds_s[buf][g][32 * half + 16 * s + 4 * kb]); };
+      auto vs = [&](int s, int g) { return *reinterpret_cast<const f4*>(&lds_s[buf][G + g][32 * half + 16 * s + 4 * kb]); };
+      auto there = [&](int s) { return (bits >> s & 1) != 0; };
+      const bool masked = first < see.all_lo || first + 32 > see.all_hi || bits != 3;
+      rows.template step<BF>(first, kb, masked, k, v, ks, vs, there);
+    }
+    if (stage + 1 < stages) store(stage + 1);
+    __syncthreads();
+  }
+
+  rows.finish();
+#pragma unroll
+  for (int i = 0; i < NQ; ++i) {
+    if (rows.to[i] < 0) continue;
+    const bool whole = t.sh.parts == 1;
+    constexpr int kPer = R::kPer;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const int d = R::dim(4 * kb + e, g * kPer);    // kPer dimensions from here
+        if (!whole) {
+          float* to = part_row(a, t.part, rows.to[i], D) + d;
+#pragma unroll
+          for (int n = 0; n < kPer; n += 2)
+            *reinterpret_cast<float2*>(to + n) = make_float2(rows.o[i][g * kPer + n][e], rows.o[i][g * kPer + n + 1][e]);
+        } else if constexpr (kPer % 8 == 0) {
+#pragma unroll
+          for (int c = 0; c < kPer / 8; ++c) {
+            float v[8];
+#pragma unroll
+            for (int n = 0; n < 8; ++n) v[n] = rows.o[i][g * kPer + 8 * c + n][e];
+            store16(static_cast<uint16_t*>(a.y) + rows.to[i] * D + d, c, pack8<BF>(v));
+          }
+        } else {
+          uint16_t* to = static_cast<uint16_t*>(a.y) + rows.to[i] * D + d;
+#pragma unroll
+          for (int n = 0; n < kPer; n += 2)
+            *reinterpret_cast<uint32_t*>(to + n) = round16<BF>(rows.o[i][g * kPer + n][e]) |
+                                                   (uint32_t)round16<BF>(rows.o[i][g * kPer + n + 1][e]) << 16;
+        }
+      }
+    }
+    if (!whole && kb == 0) *part_ml(a, plan, t.part, rows.to[i], D) = make_float2(rows.m[i], rows.l[i]);
+  }
+}
+
+// ---- the join -------------------------------------------------------------------
 
 // The parts of each row, joined. One workgroup per row: D / 8 lanes hold its
 // dimensions, and the workgroup's slices take the parts in turn.
@@ -632,7 +861,7 @@ __global__ void __launch_bounds__(kThreads) kv4_join(Kv4AttentionArgs a, Plan pl
   constexpr int kLanes = D / 8, kSlices = kThreads / kLanes;
   __shared__ float weight[kMaxParts], wave_top[kWaves], wave_sum[kWaves];
   __shared__ float slice_o[kSlices][D];
-  const int64_t row = blockIdx.x, all_rows = a.T * a.q_heads;
+  const int64_t row = blockIdx.x;
   const int64_t token = row / a.q_heads;
   const int head = (int)(row - token * a.q_heads), heads = a.q_heads / a.cache.kv_heads;
   int64_t b;
@@ -652,13 +881,13 @@ __global__ void __launch_bounds__(kThreads) kv4_join(Kv4AttentionArgs a, Plan pl
   const int rows = seq.n * heads;
   const int row0 = (int)((tok * heads + head % heads) / plan.rows) * plan.rows;
   const int last = min(rows, row0 + plan.rows) - 1;
-  const Share sh = share(a, seq, row0 / heads, last / heads, plan.parts, plan.least);
+  const Share sh = share(a, plan, seq, row0 / heads, last / heads);
   if (sh.parts == 1) return;            // written by its workgroup
   const int c = threadIdx.x % kLanes, slice = threadIdx.x / kLanes, wave = threadIdx.x >> 6;
 
   float m = kLeast, l = 0.0f;
   if ((int)threadIdx.x < sh.parts) {
-    const float2 ml = reinterpret_cast<const float2*>(a.workspace + plan.parts * all_rows * D)[threadIdx.x * all_rows + row];
+    const float2 ml = *part_ml(a, plan, threadIdx.x, row, D);
     m = ml.x;
     l = ml.y;
   }
@@ -685,7 +914,7 @@ __global__ void __launch_bounds__(kThreads) kv4_join(Kv4AttentionArgs a, Plan pl
   for (int e = 0; e < 8; ++e) out[e] = 0.0f;
 #pragma unroll 2
   for (int p = slice; p < sh.parts; p += kSlices) {
-    const float* po = a.workspace + (p * all_rows + row) * D + 8 * c;
+    const float* po = part_row(a, p, row, D) + 8 * c;
     const f4 u = *reinterpret_cast<const f4*>(po), w = *reinterpret_cast<const f4*>(po + 4);
     const float g = weight[p];
     if (g != 0.0f) {                    // a part without a visible token holds nothing
@@ -715,32 +944,30 @@ __global__ void __launch_bounds__(kThreads) kv4_join(Kv4AttentionArgs a, Plan pl
 
 // ---- the launch -------------------------------------------------------------------
 
-constexpr int kPrefillTiles = 2;        // NQ of a wave with rows of its own
-
 bool split_tokens(int64_t T, int64_t B, int heads) { return T * heads <= 32 * B; }
 
-Plan plan_of(int64_t T, int64_t B, int q_heads, int kv_heads, int64_t capacity, bool ragged) {
+Plan plan_of(int64_t T, int64_t B, int q_heads, int kv_heads, int head_dim, int groups, int64_t capacity, bool ragged) {
   const int heads = q_heads / kv_heads;
   const bool split = split_tokens(T, B, heads);
   Plan p;
-  p.rows = split ? 16 : kWaves * 16 * kPrefillTiles;
-  p.tiles_per = (T / std::max<int64_t>(B, 1) * heads + p.rows - 1) / p.rows;
+  p.rows = split ? 16 : kWaves * 16 * row_tiles(head_dim, groups);
+  p.unit = split ? kTokens : stage_tokens(head_dim);
+  p.least = split ? kWaves : 512 / p.unit;
+  p.tiles_per = (T / B * heads + p.rows - 1) / p.rows;
   p.slots = ragged ? T * heads / p.rows + B : B * p.tiles_per;
-  p.least = split ? kWaves : 16;
-  const int64_t steps = (capacity + kTokens - 1) / kTokens;
-  const int64_t groups = std::max<int64_t>(p.slots * kv_heads, 1), want = split ? 2048 : 512;
-  p.parts = (int)std::max<int64_t>(1, std::min<int64_t>({(want + groups - 1) / groups, (steps + p.least - 1) / p.least, kMaxParts}));
+  const int64_t steps = (capacity + p.unit - 1) / p.unit;
+  const int64_t tiles = std::max<int64_t>(p.slots * kv_heads, 1), want = split ? 2048 : 512;
+  p.parts = (int)std::max<int64_t>(1, std::min<int64_t>({(want + tiles - 1) / tiles, (steps + p.least - 1) / p.least,
+                                                         kMaxParts}));
   return p;
 }
 
 template <int D, int G, bool BF>
 void launch_attention_t(const Kv4AttentionArgs& a, const Plan& p, hipStream_t st) {
   const dim3 grid((unsigned)(p.slots * p.parts * a.cache.kv_heads)), block(kThreads);
-  if (p.rows == 16) kv4_attention<D, G, BF, 1, true><<<grid, block, 0, st>>>(a, p);
-  else kv4_attention<D, G, BF, kPrefillTiles, false><<<grid, block, 0, st>>>(a, p);
-  if (p.parts > 1) {
-    kv4_join<D, BF><<<dim3((unsigned)(a.T * a.q_heads)), block, 0, st>>>(a, p);
-  }
+  if (p.rows == 16) kv4_tokens<D, G, BF><<<grid, block, 0, st>>>(a, p);
+  else kv4_rows<D, G, BF><<<grid, block, 0, st>>>(a, p);
+  if (p.parts > 1) kv4_join<D, BF><<<dim3((unsigned)(a.T * a.q_heads)), block, 0, st>>>(a, p);
 }
 
 template <bool BF>
@@ -759,9 +986,9 @@ void launch_attention_d(const Kv4AttentionArgs& a, const Plan& p, hipStream_t st
 
 }  // namespace
 
-bool kv4_attention_fits(int64_t T, int64_t B, int q_heads, int kv_heads, int64_t capacity) {
-  for (const bool ragged : {false, true}) {
-    const Plan p = plan_of(T, B, q_heads, kv_heads, capacity, ragged);
+bool kv4_attention_fits(int64_t T, int64_t B, int q_heads, int kv_heads, int head_dim, int64_t capacity) {
+  for (int i = 0; i < 6; ++i) {
+    const Plan p = plan_of(T, B, q_heads, kv_heads, head_dim, 1 << i / 2, capacity, i % 2);
     if (p.slots * p.parts * kv_heads * kThreads >= (int64_t(1) << 31)) return false;
     if (p.parts > 1 && T * q_heads * kThreads >= (int64_t(1) << 31)) return false;
   }
@@ -769,13 +996,15 @@ bool kv4_attention_fits(int64_t T, int64_t B, int q_heads, int kv_heads, int64_t
 }
 
 int64_t kv4_attention_workspace_bytes(int64_t T, int64_t B, int q_heads, int kv_heads, int head_dim, int64_t capacity) {
-  int parts = 1;                        // the call may come with or without query_offsets
-  for (const bool ragged : {false, true}) parts = std::max(parts, plan_of(T, B, q_heads, kv_heads, capacity, ragged).parts);
+  int parts = 1;                        // with or without query_offsets, for any groups
+  for (int i = 0; i < 6; ++i)
+    parts = std::max(parts, plan_of(T, B, q_heads, kv_heads, head_dim, 1 << i / 2, capacity, i % 2).parts);
   return parts > 1 ? parts * T * q_heads * (head_dim + 2) * (int64_t)sizeof(float) : 0;
 }
 
 hipError_t launch_kv4_attention(const Kv4AttentionArgs& a, bool bf16, hipStream_t stream) {
-  const Plan p = plan_of(a.T, a.B, a.q_heads, a.cache.kv_heads, a.max_pages << a.cache.page_shift, a.query_offsets != nullptr);
+  const Plan p = plan_of(a.T, a.B, a.q_heads, a.cache.kv_heads, a.cache.head_dim, a.cache.groups,
+                         a.max_pages << a.cache.page_shift, a.query_offsets != nullptr);
   bf16 ? launch_attention_d<true>(a, p, stream) : launch_attention_d<false>(a, p, stream);
   return hipGetLastError();
 }
