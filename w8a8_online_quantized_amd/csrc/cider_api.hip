@@ -856,7 +856,7 @@ cider_status_t cider_kv4_attention(const cider_kv4_attention_t* args, void* stre
   if (!device_is_gfx950()) return CIDER_ERROR_NOT_SUPPORTED;
   // a window that reaches over the whole capacity hides nothing
   const cider::Kv4AttentionArgs k{kv4_cache_of(c), a.q, a.page_table, a.lengths, a.query_offsets, a.y,
-                                  static_cast<float*>(a.workspace), a.T, a.B, a.max_pages, a.q_row_stride,
+                                  need > 0 ? static_cast<float*>(a.workspace) : nullptr, a.T, a.B, a.max_pages, a.q_row_stride,
                                   a.q_head_stride, a.q_heads, a.causal, a.window < capacity ? a.window : 0,
                                   a.softmax_scale};
   return from_hip(cider::launch_kv4_attention(k, a.dtype == CIDER_DTYPE_BF16, static_cast<hipStream_t>(stream)));

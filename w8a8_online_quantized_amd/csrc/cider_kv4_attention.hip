@@ -70,6 +70,10 @@ __device__ __forceinline__ float uniform(float v) {
   return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, v)));
 }
 
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  return (int64_t)(uint32_t)uniform((int)v) | (int64_t)uniform((int)(v >> 32)) << 32;
+}
+
 typedef __attribute__((address_space(1))) const uint8_t gbyte;
 
 template <typename T>
@@ -77,7 +81,7 @@ __device__ __forceinline__ T gload(gbyte* p) { return *(__attribute__((address_s
 
 // ---- which rows and tokens a workgroup has ------------------------------------
 
-// The launch: how rows are tiled and tokens split (the same in the join).
+// The launch of kv4_rows: how rows are tiled and tokens split (the same in its join).
 struct Plan {
   int rows;            // of a workgroup's tile
   int unit;            // tokens of one step of a workgroup's loop
@@ -209,16 +213,24 @@ __device__ __forceinline__ int page_at(const Kv4AttentionArgs& a, int64_t b, int
 
 // ---- the operands ---------------------------------------------------------------
 
+// A nibble as an operand: mask, then the exponent of 64 (fp16) or 128 (bf16). The
+// constants stay in registers: v_and_or_b32 takes no literals, and v_and and v_or
+// with theirs are two instructions.
+struct Nibbles {
+  uint32_t mask, one;
+};
+template <bool BF>
+__device__ __forceinline__ Nibbles nibbles() {
+  Nibbles c{BF ? 0x000F000Fu : 0x00F000F0u, BF ? 0x43004300u : 0x54005400u};
+  asm("" : "+s"(c.mask), "+v"(c.one));
+  return c;
+}
 // 8 nibbles of a word as an operand: elements in the order 0 4 1 5 2 6 3 7.
 template <bool BF>
-__device__ __forceinline__ u4 k_operand(uint32_t w) {
-  if constexpr (BF) {
-    constexpr uint32_t kMask = 0x000F000Fu, kOne = 0x43004300u;      // 128 + n
-    return u4{(w & kMask) | kOne, ((w >> 4) & kMask) | kOne, ((w >> 8) & kMask) | kOne, ((w >> 12) & kMask) | kOne};
-  } else {
-    constexpr uint32_t kMask = 0x00F000F0u, kOne = 0x54005400u;      // 64 + n
-    return u4{((w << 4) & kMask) | kOne, (w & kMask) | kOne, ((w >> 4) & kMask) | kOne, ((w >> 8) & kMask) | kOne};
-  }
+__device__ __forceinline__ u4 k_operand(uint32_t w, Nibbles c) {
+  const auto pick = [&](uint32_t v) { return (v & c.mask) | c.one; };
+  if constexpr (BF) return u4{pick(w), pick(w >> 4), pick(w >> 8), pick(w >> 12)};      // 128 + n
+  else return u4{pick(w << 4), pick(w), pick(w >> 4), pick(w >> 8)};                    // 64 + n
 }
 // 16-bit elements 0 .. 7 in that order.
 __device__ __forceinline__ u4 k_order(u4 q) {
@@ -226,8 +238,9 @@ __device__ __forceinline__ u4 k_order(u4 q) {
             __builtin_amdgcn_perm(q.w, q.y, 0x05040100u), __builtin_amdgcn_perm(q.w, q.y, 0x07060302u)};
 }
 // Nibble n of the 16-bit halves of four words (tokens 2i, 2i + 1) as an operand 64 + n.
-__device__ __forceinline__ u4 v_operand(u4 w, int n) {
-  return ((n == 0 ? w << 4 : w >> (4 * n - 4)) & 0x00F000F0u) | 0x54005400u;
+__device__ __forceinline__ u4 v_operand(u4 w, int n, Nibbles c) {
+  const auto pick = [&](uint32_t v) { return ((n == 0 ? v << 4 : v >> (4 * n - 4)) & c.mask) | c.one; };
+  return u4{pick(w.x), pick(w.y), pick(w.z), pick(w.w)};
 }
 
 // A power of two above v (from 2^-126 to 2^126), and the inverse of such a one.
@@ -437,6 +450,38 @@ __device__ __forceinline__ float2* part_ml(const Kv4AttentionArgs& a, const Plan
 }
 
 // ---- few rows -------------------------------------------------------------------
+//
+// The launch has a fixed number of workgroups, and each takes an equal share of
+// all the work: rounds of 128 tokens (one step per wave) of one tile of rows and
+// one key/value head ("segment"), in the order of sequences, heads, tiles. A
+// workgroup may so end one segment, have some of its own, and begin another; what
+// it has not alone goes to the workspace, and the workgroup in which a segment
+// began notes there where its other parts are.
+
+constexpr int kRoundTokens = kTokens * kWaves;
+
+// A segment that began in workgroup i (entry i): its parts are that workgroup's
+// second partial result and the first ones of the next parts - 1.
+struct Note {
+  int parts, q0, h, row0, rows;        // parts 0: none; rows: of the tile, rows there are
+  int pad[3];
+};
+
+// Workspace: notes [blocks], then partial results [blocks][2][16] rows of fp32
+// averages [D], then their (m, l).
+__device__ __forceinline__ float* piece_row(const Kv4AttentionArgs& a, int blocks, int64_t piece, int row, int D) {
+  return a.workspace + blocks * 8 + (piece * 16 + row) * D;
+}
+__device__ __forceinline__ float2* piece_ml(const Kv4AttentionArgs& a, int blocks, int64_t piece, int row, int D) {
+  return reinterpret_cast<float2*>(a.workspace + blocks * 8 + (int64_t)blocks * 32 * D) + piece * 16 + row;
+}
+
+// Rounds of each of a sequence's segments, and how many segments it has.
+__device__ __forceinline__ int rounds_of(const Kv4AttentionArgs& a, const Sequence& s) {
+  const int begin = (a.window ? max(0, s.length - s.n - a.window + 1) : 0) & ~(kTokens - 1);
+  return s.length > begin ? (s.length - begin + kRoundTokens - 1) / kRoundTokens : 1;   // rows of zeros take one, too
+}
+__device__ __forceinline__ int tiles_of(const Sequence& s, int heads) { return (int)(((int64_t)s.n * heads + 15) / 16); }
 
 // One step's 32 tokens as loaded: a lane has the codes of its K row (l16) and of
 // its sixteenth of eight V rows, and one token's scale of K (lanes 0 .. 31) or V.
@@ -448,8 +493,14 @@ struct Raw {
   float s[G];
 };
 
+// Steps of kv4_tokens in registers, and workgroups that a CU then holds at once.
+// (D = 256 needs more than 256 registers: one wave per SIMD 35.5 us for 24 requests
+// of 5 queries in a window of 3000, two with spills 54.7).
+constexpr int ring_steps(int D) { return D == 256 ? 2 : 3; }
+constexpr int tokens_per_cu(int D) { return D == 256 ? 1 : 2; }
+
 template <int D, int G, bool BF>
-__global__ void __launch_bounds__(kThreads, D == 256 ? 2 : G == 4 ? 2 : 3) kv4_tokens(Kv4AttentionArgs a, Plan plan) {
+__global__ void __launch_bounds__(kThreads, tokens_per_cu(D)) kv4_tokens(Kv4AttentionArgs a, int blocks) {
   using R = Rows<D, G, 1>;
   constexpr int kSteps = R::kSteps, kPitch = D + 4;
   union Shared {
@@ -457,19 +508,121 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : G == 4 ? 2 : 3) kv4_t
       float o[kWaves][16][kPitch], m[kWaves][16], l[kWaves][16];
     } out;
     float s[kWaves][G][64];              // a step's scales, each wave its own
+    struct {
+      int64_t sum[kWaves], before, b;
+    } plan;
   };
   __shared__ Shared shared;
   const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
   const int l16 = lane & 15, kb = lane >> 4;
-  Tile t;
-  if (!find_tile(a, plan, lane, t)) return;
-  R rows;
-  rows.template begin<BF>(a, t, t.row0, lane);
-  const Sight see = sight(a, t, t.row0, 16);
-  const int step_end = min(t.sh.steps, (t.part + 1) * t.sh.per);
-  const int first_token = t.sh.begin & ~(kTokens - 1);
+  const int hkv = a.cache.kv_heads, heads = a.q_heads / hkv;
+  // one XCD's workgroups are neighbours in the work, so that a head's tiles share its L2
+  const int block = blocks % 8 ? (int)blockIdx.x : (int)(blockIdx.x % 8) * (blocks / 8) + (int)blockIdx.x / 8;
+  Note* const note = reinterpret_cast<Note*>(a.workspace) + block;
+
+  // ---- the share: rounds [pos, pos_end) of all
+  auto work_of = [&](int64_t b) {
+    const Sequence q = sequence(a, b);
+    return (int64_t)tiles_of(q, heads) * hkv * rounds_of(a, q);
+  };
+  auto scan = [&](int64_t v, int64_t& total) {          // inclusive sums over the workgroup
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int64_t up = __shfl_up(v, off);
+      if (lane >= off) v += up;
+    }
+    __syncthreads();
+    if (lane == 63) shared.plan.sum[wave] = v;
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      if (w < wave) v += shared.plan.sum[w];
+      total += shared.plan.sum[w];
+    }
+    return v;
+  };
+  int64_t all = 0;
+  int64_t mine = 0, upto = 0;            // of sequence threadIdx.x, kept when there are no more
+  for (int64_t b0 = 0; b0 < a.B; b0 += kThreads) {
+    mine = b0 + threadIdx.x < a.B ? work_of(b0 + threadIdx.x) : 0;
+    int64_t total;
+    upto = scan(mine, total);
+    all += uniform(total);
+  }
+  const int64_t share = (all + blocks - 1) / blocks;
+  int64_t pos = block * share;
+  const int64_t pos_end = min(all, pos + share);
+  if (pos >= pos_end) {
+    if (a.workspace && threadIdx.x == 0) note->parts = 0;
+    return;
+  }
+  {
+    int64_t before = 0;
+    for (int64_t b0 = 0; b0 < a.B; b0 += kThreads) {
+      int64_t total = all;
+      if (a.B > kThreads) {
+        mine = b0 + threadIdx.x < a.B ? work_of(b0 + threadIdx.x) : 0;
+        upto = scan(mine, total);
+      }
+      if (before + upto > pos && before + upto - mine <= pos) {
+        shared.plan.before = before + upto - mine;
+        shared.plan.b = b0 + threadIdx.x;
+      }
+      if (before + total > pos) break;
+      before += uniform(total);
+    }
+  }
+  __syncthreads();
+  int64_t b = uniform((int)shared.plan.b);
+  int in_b = uniform((int)(pos - shared.plan.before));  // rounds of this sequence before pos: below 2^31
+  __syncthreads();
+
   const float scale = a.softmax_scale * kLog2e;
-  const int page_size = a.cache.page_size, hkv = a.cache.kv_heads;
+  const int page_size = a.cache.page_size;
+  const Nibbles k_nib = nibbles<BF>(), v_nib = nibbles<false>();
+
+  // ---- a segment, or the part of it that is in the share
+  struct Segment {
+    Tile t;
+    Sight see;
+    int rounds, first_round, n_rounds;   // of the segment; those in the share
+    int64_t began;                       // the first of those, of all
+    int first_token, step, step_end;     // this wave's steps, kWaves apart
+  } seg;
+  Sequence seq = sequence(a, b);
+  auto next = [&]() {
+    if (pos >= pos_end) return false;
+    int tiles;
+    while (true) {
+      tiles = tiles_of(seq, heads);
+      seg.rounds = rounds_of(a, seq);
+      if (in_b < tiles * hkv * seg.rounds) break;
+      in_b -= tiles * hkv * seg.rounds;  // the next sequence (this one may have no queries)
+      seq = sequence(a, ++b);
+    }
+    const int which = in_b / seg.rounds;
+    seg.first_round = in_b - which * seg.rounds;
+    seg.n_rounds = (int)min((int64_t)(seg.rounds - seg.first_round), pos_end - pos);
+    seg.began = pos;
+    in_b += seg.n_rounds;
+    pos += seg.n_rounds;
+    Tile& t = seg.t;
+    t.heads = heads;
+    t.b = b;
+    t.seq = seq;
+    t.rows = seq.n * heads;
+    t.h = which / tiles;
+    t.row0 = (which - t.h * tiles) * 16;
+    seg.see = sight(a, t, t.row0, 16);
+    // (a sequence's segments all begin where its first query's window does)
+    seg.first_token = ((a.window ? max(0, seq.length - seq.n - a.window + 1) : 0) & ~(kTokens - 1)) +
+                      seg.first_round * kRoundTokens;
+    seg.step_end = min(seg.n_rounds * kWaves, (seg.see.any_hi - seg.first_token + kTokens - 1) / kTokens);
+    seg.step = wave;
+    if (seg.see.any_lo > seg.first_token) seg.step += (seg.see.any_lo - seg.first_token) / kRoundTokens * kWaves;
+    return true;
+  };
 
   const uint32_t k_lane = l16 * (D / 2) + kb * (D / G / 8), v_lane = 4 * kb * (D / 2) + l16 * (D / 32);
   auto load = [&](int token, const int (&pages)[2], Raw<D, G>& r) {
@@ -479,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : G == 4 ? 2 : 3) kv4_t
     for (int s = 0; s < 2; ++s) {
       const bool there = pages[s] >= 0;
       at[s] = there ? (token + 16 * s) & (page_size - 1) : 0;
-      ph[s] = (int64_t)(there ? pages[s] : 0) * hkv + t.h;
+      ph[s] = (int64_t)(there ? pages[s] : 0) * hkv + seg.t.h;
       const int64_t base = (ph[s] * page_size + at[s]) * (D / 2);
       gbyte* k = (gbyte*)a.cache.k_codes + base;      // uniform; the lane's part is a 32-bit offset
 #pragma unroll
@@ -521,7 +674,9 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : G == 4 ? 2 : 3) kv4_t
     for (int g = 0; g < G; ++g) r.s[g] = gload<float>(from + (so + g * page_size) * 4);
   };
 
+  R rows;
   auto process = [&](int token, const int (&pages)[2], Raw<D, G>& r) {
+    const Sight& see = seg.see;
     const bool masked = token < see.all_lo || token + kTokens > see.all_hi || pages[0] < 0 || pages[1] < 0;
     if (masked) {
       // scales that no row may see are nothing
@@ -541,100 +696,200 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : G == 4 ? 2 : 3) kv4_t
       }
       shared.s[wave][g][lane] = r.s[g] * (lane < 32 ? scale : power_inverse(rows.ref[g]));
     }
-    auto k = [&](int s, int st) { return k_operand<BF>(r.k[s][st]); };
+    auto k = [&](int s, int st) { return k_operand<BF>(r.k[s][st], k_nib); };
     u4 w[D / 64];
 #pragma unroll
     for (int c = 0; c < D / 64; ++c)
 #pragma unroll
       for (int pr = 0; pr < 4; ++pr)
         w[c][pr] = __builtin_amdgcn_perm(r.v[2 * pr + 1][c / 2], r.v[2 * pr][c / 2], c % 2 ? 0x07060302u : 0x05040100u);
-    auto v = [&](int j) { return v_operand(w[j / 4], j % 4); };
+    auto v = [&](int j) { return v_operand(w[j / 4], j % 4, v_nib); };
     auto ks = [&](int s, int g) { return *reinterpret_cast<const f4*>(&shared.s[wave][g][16 * s + 4 * kb]); };
     auto vs = [&](int s, int g) { return *reinterpret_cast<const f4*>(&shared.s[wave][g][32 + 16 * s + 4 * kb]); };
     auto there = [&](int s) { return s ? pages[1] >= 0 : pages[0] >= 0; };
     rows.template step<BF>(token, kb, masked, k, v, ks, vs, there);
   };
 
-  // the waves take the steps in turn, the next one's codes on their way during each
-  {
-    int step = t.part * t.sh.per + wave;
-    // the pages of 32 steps, a lane each, so that no step waits for a table entry
-    auto pages_from = [&](int first) {
-      return page_at(a, t.b, first_token + (first + (lane >> 1) * kWaves) * kTokens + (lane & 1) * 16, see.any_hi);
-    };
-    if (step < step_end) {
-      int ids = pages_from(step), at = 0;         // `at`: the sub-tile of ids that comes next
-      auto take = [&](int (&p)[2]) {
-        p[0] = __builtin_amdgcn_readlane(ids, at);
-        p[1] = __builtin_amdgcn_readlane(ids, at + 1);
-        at += 2;
-      };
-      int pages[2], next[2];
-      Raw<D, G> cur, nxt;
-      take(pages);
-      load(first_token + step * kTokens, pages, cur);
-      for (; step < step_end; step += kWaves) {
-        if (step + kWaves < step_end) {
-          if (at == 64) {
-            ids = pages_from(step + kWaves);
-            at = 0;
-          }
-          take(next);
-          load(first_token + (step + kWaves) * kTokens, next, nxt);
-        }
-        process(first_token + step * kTokens, pages, cur);
-        cur = nxt;
-        pages[0] = next[0];
-        pages[1] = next[1];
-      }
+  // The pages of 32 steps, a lane each, so that no step waits for a table entry.
+  auto pages_from = [&](int first) {
+    return page_at(a, seg.t.b, seg.first_token + (first + (lane >> 1) * kWaves) * kTokens + (lane & 1) * 16, seg.see.any_hi);
+  };
+  int ids = 0, at = 0;                   // `at`: the sub-tile of ids that comes next
+  int ahead = 0;                         // the step whose codes are loaded next
+  struct Step {
+    int token, pages[2];
+    Raw<D, G> raw;
+  };
+  // kRing steps in registers: the others on their way while one is worked on. The
+  // loads are unconditional (past the end, of the last codes again): behind a branch
+  // the wait for one step's would be one for all in flight.
+  constexpr int kRing = ring_steps(D);
+  Step ring[kRing];
+  auto fetch = [&](Step& to) {
+    if (at == 64) {
+      ids = pages_from(ahead);
+      at = 0;
     }
-  }
+    to.pages[0] = __builtin_amdgcn_readlane(ids, at);
+    to.pages[1] = __builtin_amdgcn_readlane(ids, at + 1);
+    to.token = seg.first_token + ahead * kTokens;
+    load(to.token, to.pages, to.raw);
+    if (ahead + kWaves < seg.step_end) {
+      ahead += kWaves;
+      at += 2;
+    }
+  };
+  auto fetch_first = [&]() {
+    ids = pages_from(seg.step);
+    at = 0;
+    ahead = seg.step;
+#pragma unroll
+    for (int i = 0; i + 1 < kRing; ++i) fetch(ring[i]);
+  };
 
-  // the waves' parts of each row, joined
-  rows.finish();
-  __syncthreads();                       // every wave is done with its scales
-  if (kb == 0) {
-    shared.out.m[wave][l16] = rows.m[0];
-    shared.out.l[wave][l16] = rows.l[0];
-  }
+  bool noted = false;
+  next();
+  fetch_first();
+  while (true) {
+    rows.template begin<BF>(a, seg.t, seg.t.row0, lane);       // its loads behind the first codes'
+    bool more = seg.step < seg.step_end;
+    while (more) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-#pragma unroll
-    for (int j = 0; j < R::kTiles; ++j) shared.out.o[wave][l16][R::dim(4 * kb + e, j)] = rows.o[0][j][e];
-  __syncthreads();
-  constexpr int kChunks = D / 8;
-  const int n_rows = min(16, t.rows - t.row0);
-  for (int item = threadIdx.x; item < n_rows * kChunks; item += kThreads) {
-    const int r = item / kChunks, c = item - r * kChunks;
-    float top = kLeast;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) top = __builtin_fmaxf(top, shared.out.m[w][r]);
-    float sum = 0.0f, out[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) out[e] = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      const float f = __builtin_amdgcn_exp2f(shared.out.m[w][r] - top) * shared.out.l[w][r];
-      sum += f;
-      if (f != 0.0f) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) out[e] = __builtin_fmaf(f, shared.out.o[w][r][8 * c + e], out[e]);
+      for (int i = 0; i < kRing; ++i) {
+        fetch(ring[(i + kRing - 1) % kRing]);
+        process(ring[i].token, ring[i].pages, ring[i].raw);
+        seg.step += kWaves;
+        more = seg.step < seg.step_end;
+        if (!more) break;
       }
     }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    // the next segment's first codes are on their way while this one is finished
+    const Segment done = seg;
+    const bool again = next();
+    if (again) fetch_first();
+
+    // the waves' parts of each row, joined
+    const Tile& t = done.t;
+    const bool whole = done.n_rounds == done.rounds;
+    rows.finish();
+    __syncthreads();                       // every wave is done with its scales
+    if (kb == 0) {
+      shared.out.m[wave][l16] = rows.m[0];
+      shared.out.l[wave][l16] = rows.l[0];
+    }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) out[e] *= inv;
-    const int tok = (t.row0 + r) / t.heads;
-    const int64_t to = (t.seq.q0 + tok) * a.q_heads + t.h * t.heads + (t.row0 + r) - tok * t.heads;
-    if (t.sh.parts == 1) {
-      store16(static_cast<uint16_t*>(a.y) + to * D, c, pack8<BF>(out));
-    } else {
-      float* po = part_row(a, t.part, to, D) + 8 * c;
-      *reinterpret_cast<f4*>(po) = f4{out[0], out[1], out[2], out[3]};
-      *reinterpret_cast<f4*>(po + 4) = f4{out[4], out[5], out[6], out[7]};
-      if (c == 0) *part_ml(a, plan, t.part, to, D) = make_float2(top, sum);
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int j = 0; j < R::kTiles; ++j) shared.out.o[wave][l16][R::dim(4 * kb + e, j)] = rows.o[0][j][e];
+    __syncthreads();
+    constexpr int kChunks = D / 8;
+    const int n_rows = min(16, t.rows - t.row0);
+    for (int item = threadIdx.x; item < n_rows * kChunks; item += kThreads) {
+      const int r = item / kChunks, c = item - r * kChunks;
+      float top = kLeast;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) top = __builtin_fmaxf(top, shared.out.m[w][r]);
+      float sum = 0.0f, out[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) out[e] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const float f = __builtin_amdgcn_exp2f(shared.out.m[w][r] - top) * shared.out.l[w][r];
+        sum += f;
+        if (f != 0.0f) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) out[e] = __builtin_fmaf(f, shared.out.o[w][r][8 * c + e], out[e]);
+        }
+      }
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) out[e] *= inv;
+      const int tok = (t.row0 + r) / t.heads;
+      const int64_t to = (t.seq.q0 + tok) * a.q_heads + t.h * t.heads + (t.row0 + r) - tok * t.heads;
+      if (whole) {
+        store16(static_cast<uint16_t*>(a.y) + to * D, c, pack8<BF>(out));
+      } else {
+        const int64_t piece = 2 * (int64_t)block + (done.first_round == 0);
+        float* po = piece_row(a, blocks, piece, r, D) + 8 * c;
+        *reinterpret_cast<f4*>(po) = f4{out[0], out[1], out[2], out[3]};
+        *reinterpret_cast<f4*>(po + 4) = f4{out[4], out[5], out[6], out[7]};
+        if (c == 0) *piece_ml(a, blocks, piece, r, D) = make_float2(top, sum);
+      }
+    }
+    if (!whole && done.first_round == 0) {
+      noted = true;
+      if (threadIdx.x == 0) {
+        const int64_t last = (done.began + done.rounds - 1) / share;      // the workgroup of its last round
+        note->parts = (int)(last - block) + 1;
+        note->q0 = (int)t.seq.q0;
+        note->h = t.h;
+        note->row0 = t.row0;
+        note->rows = n_rows;
+      }
+    }
+    if (!again) break;
+    __syncthreads();                     // the next segment's scales take the place of these sums
+  }
+  if (a.workspace && !noted && threadIdx.x == 0) note->parts = 0;
+}
+
+// The pieces of one row of the segment that began in workgroup blockIdx.x, joined:
+// D / 8 lanes hold its dimensions, and the workgroup's slices take the pieces in turn.
+template <int D, bool BF>
+__global__ void __launch_bounds__(kThreads) kv4_join_pieces(Kv4AttentionArgs a, int blocks) {
+  constexpr int kLanes = D / 8, kSlices = kThreads / kLanes;
+  __shared__ float slice_o[kSlices][D], slice_sum[kSlices], wave_top[kWaves];
+  const int block = blockIdx.x, r = blockIdx.y;
+  const Note note = reinterpret_cast<const Note*>(a.workspace)[block];
+  if (note.parts == 0 || r >= note.rows) return;
+  const int c = threadIdx.x % kLanes, slice = threadIdx.x / kLanes;
+  auto piece = [&](int p) { return p == 0 ? 2 * (int64_t)block + 1 : 2 * (int64_t)(block + p); };
+  float top = kLeast;
+  for (int p = threadIdx.x; p < note.parts; p += kThreads)
+    top = __builtin_fmaxf(top, piece_ml(a, blocks, piece(p), r, D)->x);
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, off));
+  if ((threadIdx.x & 63) == 0) wave_top[threadIdx.x >> 6] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) top = __builtin_fmaxf(top, wave_top[w]);
+  float sum = 0.0f, out[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) out[e] = 0.0f;
+#pragma unroll 4
+  for (int p = slice; p < note.parts; p += kSlices) {
+    const float2 ml = *piece_ml(a, blocks, piece(p), r, D);
+    const float* po = piece_row(a, blocks, piece(p), r, D) + 8 * c;
+    const f4 u = *reinterpret_cast<const f4*>(po), w = *reinterpret_cast<const f4*>(po + 4);
+    const float g = __builtin_amdgcn_exp2f(ml.x - top) * ml.y;
+    sum += g;
+    if (g != 0.0f) {                    // a piece without a visible token holds nothing
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        out[e] = __builtin_fmaf(g, u[e], out[e]);
+        out[4 + e] = __builtin_fmaf(g, w[e], out[4 + e]);
+      }
     }
   }
+  const int used = min(kSlices, note.parts);
+  if (slice > 0 && slice < used) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) slice_o[slice][8 * c + e] = out[e];
+    if (c == 0) slice_sum[slice] = sum;
+  }
+  __syncthreads();
+  if (slice > 0) return;
+  for (int s = 1; s < used; ++s) {
+    sum += slice_sum[s];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) out[e] += slice_o[s][8 * c + e];
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) out[e] *= inv;
+  const int hkv = a.cache.kv_heads, heads = a.q_heads / hkv, tok = (note.row0 + r) / heads;
+  const int64_t to = ((int64_t)note.q0 + tok) * a.q_heads + note.h * heads + (note.row0 + r) - tok * heads;
+  store16(static_cast<uint16_t*>(a.y) + to * D, c, pack8<BF>(out));
 }
 
 // ---- many rows ------------------------------------------------------------------
@@ -668,6 +923,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_rows(Kv4AttentionArgs a, Plan
   const int first_token = (t.sh.begin & ~(S - 1)) + stage0 * S;
   const float scale = a.softmax_scale * kLog2e;
   const int page_size = a.cache.page_size, hkv = a.cache.kv_heads;
+  const Nibbles k_nib = nibbles<BF>(), v_nib = nibbles<false>();
 
   // ---- staging: codes and scales of the next stage in registers
   const int k_sub = wave % kSubs, k_step = wave / kSubs * kKPer;
@@ -752,17 +1008,17 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_rows(Kv4AttentionArgs a, Plan
   auto store = [&](int stage) {
     const int buf = stage & 1;
 #pragma unroll
-    for (int i = 0; i < kKPer; ++i) lds_k[buf][k_sub][k_step + i][lane] = k_operand<BF>(raw_k[i]);
+    for (int i = 0; i < kKPer; ++i) lds_k[buf][k_sub][k_step + i][lane] = k_operand<BF>(raw_k[i], k_nib);
     u4 w;
 #pragma unroll
     for (int pr = 0; pr < 4; ++pr) w[pr] = raw_v[2 * pr] | raw_v[2 * pr + 1] << 16;
     if constexpr (kVPer == 4) {
 #pragma unroll
-      for (int n = 0; n < 4; ++n) lds_v[buf][v_half][v_tile + n][lane] = v_operand(w, n);
+      for (int n = 0; n < 4; ++n) lds_v[buf][v_half][v_tile + n][lane] = v_operand(w, n, v_nib);
     } else {                             // half of the four tiles of these 16 bits
       if (v_tile % 4) w >>= 8;
 #pragma unroll
-      for (int n = 0; n < 2; ++n) lds_v[buf][v_half][v_tile + n][lane] = v_operand(w, n);
+      for (int n = 0; n < 2; ++n) lds_v[buf][v_half][v_tile + n][lane] = v_operand(w, n, v_nib);
     }
 #pragma unroll
     for (int i = 0; i < (kArrays + kWaves - 1) / kWaves; ++i) {
@@ -944,58 +1200,87 @@ __global__ void __launch_bounds__(kThreads) kv4_join(Kv4AttentionArgs a, Plan pl
 
 // ---- the launch -------------------------------------------------------------------
 
-bool split_tokens(int64_t T, int64_t B, int heads) { return T * heads <= 32 * B; }
+bool few_rows(int64_t T, int64_t B, int heads) { return T * heads <= 32 * B; }
 
 Plan plan_of(int64_t T, int64_t B, int q_heads, int kv_heads, int head_dim, int groups, int64_t capacity, bool ragged) {
   const int heads = q_heads / kv_heads;
-  const bool split = split_tokens(T, B, heads);
   Plan p;
-  p.rows = split ? 16 : kWaves * 16 * row_tiles(head_dim, groups);
-  p.unit = split ? kTokens : stage_tokens(head_dim);
-  p.least = split ? kWaves : 512 / p.unit;
+  p.rows = kWaves * 16 * row_tiles(head_dim, groups);
+  p.unit = stage_tokens(head_dim);
+  p.least = 512 / p.unit;
   p.tiles_per = (T / B * heads + p.rows - 1) / p.rows;
   p.slots = ragged ? T * heads / p.rows + B : B * p.tiles_per;
-  const int64_t steps = (capacity + p.unit - 1) / p.unit;
-  const int64_t tiles = std::max<int64_t>(p.slots * kv_heads, 1), want = split ? 2048 : 512;
-  p.parts = (int)std::max<int64_t>(1, std::min<int64_t>({(want + tiles - 1) / tiles, (steps + p.least - 1) / p.least,
+  const int64_t steps = (capacity + p.unit - 1) / p.unit, tiles = std::max<int64_t>(p.slots * kv_heads, 1);
+  p.parts = (int)std::max<int64_t>(1, std::min<int64_t>({(512 + tiles - 1) / tiles, (steps + p.least - 1) / p.least,
                                                          kMaxParts}));
   return p;
 }
 
+// Workgroups of kv4_tokens: those that are resident at once, or one per round if
+// no sequence can have so many. With one round per segment at most, nothing is
+// split and nothing joined.
+int tokens_blocks(int64_t T, int64_t B, int q_heads, int kv_heads, int head_dim, int64_t capacity) {
+  const int64_t segments = (T * (q_heads / kv_heads) / 16 + B) * kv_heads;
+  const int64_t rounds = std::max<int64_t>(1, (capacity + kTokens + kRoundTokens - 1) / kRoundTokens);
+  const int64_t most = 256 * tokens_per_cu(head_dim);
+  return (int)(segments < most ? std::min(most, segments * rounds) : most);
+}
+
 template <int D, int G, bool BF>
-void launch_attention_t(const Kv4AttentionArgs& a, const Plan& p, hipStream_t st) {
-  const dim3 grid((unsigned)(p.slots * p.parts * a.cache.kv_heads)), block(kThreads);
-  if (p.rows == 16) kv4_tokens<D, G, BF><<<grid, block, 0, st>>>(a, p);
-  else kv4_rows<D, G, BF><<<grid, block, 0, st>>>(a, p);
+void launch_attention_t(const Kv4AttentionArgs& a, hipStream_t st) {
+  const int hkv = a.cache.kv_heads, heads = a.q_heads / hkv;
+  const int64_t capacity = a.max_pages << a.cache.page_shift;
+  const dim3 block(kThreads);
+  if (few_rows(a.T, a.B, heads)) {
+    const int blocks = tokens_blocks(a.T, a.B, a.q_heads, hkv, D, capacity);
+    kv4_tokens<D, G, BF><<<dim3(blocks), block, 0, st>>>(a, blocks);
+    if (a.workspace) {
+      const unsigned rows = a.query_offsets ? 16 : (unsigned)std::min<int64_t>(16, a.T / a.B * heads);
+      kv4_join_pieces<D, BF><<<dim3(blocks, rows), block, 0, st>>>(a, blocks);
+    }
+    return;
+  }
+  const Plan p = plan_of(a.T, a.B, a.q_heads, hkv, D, G, capacity, a.query_offsets != nullptr);
+  kv4_rows<D, G, BF><<<dim3((unsigned)(p.slots * p.parts * hkv)), block, 0, st>>>(a, p);
   if (p.parts > 1) kv4_join<D, BF><<<dim3((unsigned)(a.T * a.q_heads)), block, 0, st>>>(a, p);
 }
 
 template <bool BF>
-void launch_attention_d(const Kv4AttentionArgs& a, const Plan& p, hipStream_t st) {
+void launch_attention_d(const Kv4AttentionArgs& a, hipStream_t st) {
   switch (a.cache.head_dim * 8 + a.cache.groups) {
-    case 64 * 8 + 1: launch_attention_t<64, 1, BF>(a, p, st); break;
-    case 64 * 8 + 2: launch_attention_t<64, 2, BF>(a, p, st); break;
-    case 128 * 8 + 1: launch_attention_t<128, 1, BF>(a, p, st); break;
-    case 128 * 8 + 2: launch_attention_t<128, 2, BF>(a, p, st); break;
-    case 128 * 8 + 4: launch_attention_t<128, 4, BF>(a, p, st); break;
-    case 256 * 8 + 1: launch_attention_t<256, 1, BF>(a, p, st); break;
-    case 256 * 8 + 2: launch_attention_t<256, 2, BF>(a, p, st); break;
-    default: launch_attention_t<256, 4, BF>(a, p, st); break;
+    case 64 * 8 + 1: launch_attention_t<64, 1, BF>(a, st); break;
+    case 64 * 8 + 2: launch_attention_t<64, 2, BF>(a, st); break;
+    case 128 * 8 + 1: launch_attention_t<128, 1, BF>(a, st); break;
+    case 128 * 8 + 2: launch_attention_t<128, 2, BF>(a, st); break;
+    case 128 * 8 + 4: launch_attention_t<128, 4, BF>(a, st); break;
+    case 256 * 8 + 1: launch_attention_t<256, 1, BF>(a, st); break;
+    case 256 * 8 + 2: launch_attention_t<256, 2, BF>(a, st); break;
+    default: launch_attention_t<256, 4, BF>(a, st); break;
   }
 }
 
 }  // namespace
 
 bool kv4_attention_fits(int64_t T, int64_t B, int q_heads, int kv_heads, int head_dim, int64_t capacity) {
+  constexpr int64_t kLimit = int64_t(1) << 31;
+  const int heads = q_heads / kv_heads;
+  if (few_rows(T, B, heads)) {           // a sequence's rounds are counted in 32 bits
+    return (T * heads / 16 + 1) * kv_heads * ((capacity + kTokens) / kRoundTokens + 1) < kLimit;
+  }
   for (int i = 0; i < 6; ++i) {
     const Plan p = plan_of(T, B, q_heads, kv_heads, head_dim, 1 << i / 2, capacity, i % 2);
-    if (p.slots * p.parts * kv_heads * kThreads >= (int64_t(1) << 31)) return false;
-    if (p.parts > 1 && T * q_heads * kThreads >= (int64_t(1) << 31)) return false;
+    if (p.slots * p.parts * kv_heads * kThreads >= kLimit) return false;
+    if (p.parts > 1 && T * q_heads * kThreads >= kLimit) return false;
   }
   return true;
 }
 
 int64_t kv4_attention_workspace_bytes(int64_t T, int64_t B, int q_heads, int kv_heads, int head_dim, int64_t capacity) {
+  if (few_rows(T, B, q_heads / kv_heads)) {
+    if (capacity <= kRoundTokens) return 0;            // no segment has a second round
+    const int64_t blocks = tokens_blocks(T, B, q_heads, kv_heads, head_dim, capacity);
+    return blocks * (8 + 2 * 16 * (head_dim + 2)) * (int64_t)sizeof(float);
+  }
   int parts = 1;                        // with or without query_offsets, for any groups
   for (int i = 0; i < 6; ++i)
     parts = std::max(parts, plan_of(T, B, q_heads, kv_heads, head_dim, 1 << i / 2, capacity, i % 2).parts);
@@ -1003,9 +1288,7 @@ int64_t kv4_attention_workspace_bytes(int64_t T, int64_t B, int q_heads, int kv_
 }
 
 hipError_t launch_kv4_attention(const Kv4AttentionArgs& a, bool bf16, hipStream_t stream) {
-  const Plan p = plan_of(a.T, a.B, a.q_heads, a.cache.kv_heads, a.cache.head_dim, a.cache.groups,
-                         a.max_pages << a.cache.page_shift, a.query_offsets != nullptr);
-  bf16 ? launch_attention_d<true>(a, p, stream) : launch_attention_d<false>(a, p, stream);
+  bf16 ? launch_attention_d<true>(a, stream) : launch_attention_d<false>(a, stream);
   return hipGetLastError();
 }
 
