@@ -640,7 +640,7 @@ typedef struct {
  *   of 8; q_norm, k_norm [head_dim] or NULL; positions int32 [T] and inv_freq
  *   fp64 [rotary_dim / 2] (both or neither); slots int32 [T].
  * T < 2^23, q_heads <= CIDER_KV4_MAX_Q_HEADS, rotary_dim a multiple of 16 up
- * to head_dim, eps positive and finite with a norm. */
+ * to head_dim; with a norm, eps finite and at least 2^-126. */
 typedef struct {
   cider_kv4_cache_t cache;
   const void* q;

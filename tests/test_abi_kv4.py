@@ -73,7 +73,7 @@ def append_args(cache_kw=None, **kw):
     dict(T=-1), dict(T=1 << 23), dict(q_heads=0), dict(q_heads=-1), dict(q_heads=16385), dict(dtype=2), dict(q=None),
     dict(q_out=None), dict(q=None, q_out=None), dict(k=None), dict(v=None), dict(slots=None), dict(positions=None),
     dict(inv_freq=None), dict(rotary_dim=0), dict(rotary_dim=24), dict(rotary_dim=144), dict(rotary_dim=-16),
-    dict(interleaved=2), dict(rope_scale=float("nan")), dict(eps=0.0), dict(eps=float("inf")), dict(eps=float("nan")),
+    dict(interleaved=2), dict(rope_scale=float("nan")), dict(eps=0.0), dict(eps=1e-40), dict(eps=float("inf")), dict(eps=float("nan")),
     dict(q=PTR + 8), dict(k=PTR + 8), dict(v=PTR + 2), dict(q_norm=PTR + 8), dict(k_norm=PTR + 8), dict(positions=PTR + 4),
     dict(inv_freq=PTR + 8), dict(slots=PTR + 4), dict(q_out=PTR + 8), dict(k_row_stride=252), dict(v_head_stride=-128),
     dict(q_row_stride=516), dict(out_row_stride=504), dict(out_head_stride=64), dict(q_out=PTR, out_row_stride=1024)])
@@ -141,8 +141,10 @@ def test_attention_workspace_query(L):
     assert q(0, 4, 16, 8, 128, 4096) == 0
     assert q(1, 1, 16, 8, 128, 0) == 0 and q(1, 1, 16, 8, 128, 128) == 0      # one part: no partial results
     one = q(1, 1, 16, 8, 128, 4096)
-    assert one > 0 and one % (16 * 130 * 4) == 0
+    assert one > 0 and one % 16 == 0
     assert q(1, 1, 16, 8, 128, 1 << 20) >= one                                # more tokens, more parts
+    many = q(512, 1, 16, 8, 128, 1 << 16)                                     # partial rows of 128 averages, m and l
+    assert many > 0 and many % (512 * 16 * 130 * 4) == 0
     for bad in ((-1, 1, 16, 8, 128, 64), (1, 0, 16, 8, 128, 64), (1, 1, 15, 8, 128, 64), (1, 1, 16, 0, 128, 64),
                 (1, 1, 16, 8, 96, 64), (1, 1, 16, 8, 128, -1), (1, 1, 16, 8, 128, 1 << 31), (1 << 31, 1, 16, 8, 128, 64),
                 (1 << 28, 1, 16, 8, 128, 64)):

@@ -781,7 +781,7 @@ cider_status_t cider_kv4_append(const cider_kv4_append_t* args, void* stream) {
   if (a.positions && (a.rotary_dim < 16 || a.rotary_dim % 16 || a.rotary_dim > c.head_dim ||
                       (a.interleaved != 0 && a.interleaved != 1) || !std::isfinite(a.rope_scale)))
     return CIDER_ERROR_INVALID_VALUE;
-  if ((a.q_norm || a.k_norm) && (!std::isfinite(a.eps) || !(a.eps > 0.0f))) return CIDER_ERROR_INVALID_VALUE;
+  if ((a.q_norm || a.k_norm) && (!std::isfinite(a.eps) || !(a.eps >= 0x1p-126f))) return CIDER_ERROR_INVALID_VALUE;
   if (!kv4_cache_there(c) || !a.k || !a.v || !a.slots || (a.q && a.q_heads < 1)) return CIDER_ERROR_INVALID_VALUE;
   for (const int64_t s : {a.q_row_stride, a.q_head_stride, a.k_row_stride, a.k_head_stride, a.v_row_stride,
                           a.v_head_stride, a.out_row_stride, a.out_head_stride})

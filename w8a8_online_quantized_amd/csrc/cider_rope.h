@@ -36,4 +36,12 @@ __device__ __forceinline__ void rope_pair(float& u, float& w, float2 cs) {
   w = q;
 }
 
+// One end of a pair turned, `other` being the other end and `sine` negated at the
+// first one: the same products and sum as rope_pair, so the same bits.
+__device__ __forceinline__ float rope_end(float own, float other, float cosine, float sine) {
+  float p = __builtin_fmaf(own, cosine, other * sine);
+  asm("" : "+v"(p));
+  return p;
+}
+
 }  // namespace cider
