@@ -323,10 +323,19 @@ struct Rows {
   // 32 tokens from `token` on. k(s, step), v(j): operands of sub-tile s and of
   // output tile j; ks(s, g): log2 scales of the scores of tokens 16 s + 4 kb ..,
   // vs(s, g): scales of V in units of ref. masked: not every row sees every token;
-  // there(s): sub-tile s may be read at all.
-  template <bool BF, class K, class V, class KS, class VS, class There>
+  // there(s): sub-tile s may be read at all. AHEAD: operands come from LDS, whose
+  // latency is hidden by reading several before the first is needed.
+  template <bool BF, bool AHEAD, class K, class V, class KS, class VS, class There>
   __device__ __forceinline__ void step(int token, int kb, bool masked, K k, V v, KS ks, VS vs, There there) {
     float x[NQ][8];                      // scores less m
+    u4 k_ahead[2][AHEAD ? kSteps : 1];
+    if constexpr (AHEAD && kSteps <= 4) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int st = 0; st < kSteps; ++st) k_ahead[s][st] = k(s, st);
+      __builtin_amdgcn_sched_barrier(0);
+    }
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
 #pragma unroll
@@ -336,7 +345,7 @@ struct Rows {
         for (int i = 0; i < NQ; ++i) acc[i] = f4{q_off[i][g], q_off[i][g], q_off[i][g], q_off[i][g]};
 #pragma unroll
         for (int st = 0; st < kSteps / G; ++st) {
-          const u4 op = k(s, g * (kSteps / G) + st);
+          const u4 op = AHEAD && kSteps <= 4 ? k_ahead[s][g * (kSteps / G) + st] : k(s, g * (kSteps / G) + st);
 #pragma unroll
           for (int i = 0; i < NQ; ++i) acc[i] = mfma_qk<BF>(op, q[i][g * (kSteps / G) + st], acc[i]);
         }
@@ -388,6 +397,13 @@ struct Rows {
         for (int g = 0; g < G; ++g) z[i][g] *= f;
       }
     }
+    constexpr int kAhead = AHEAD ? 4 : 1;
+    u4 v_ahead[kAhead];
+    if constexpr (AHEAD) {
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) v_ahead[j] = v(j);
+      __builtin_amdgcn_sched_barrier(0);
+    }
     u4 p16[NQ][G];
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
@@ -418,9 +434,13 @@ struct Rows {
       for (int g = 0; g < G; ++g) z[i][g] = mfma_pv(seventy_two, p16[i][g], z[i][g]);
 #pragma unroll
     for (int j = 0; j < kTiles; ++j) {
-      const u4 op = v(j);
+      const u4 op = AHEAD ? v_ahead[j % kAhead] : v(j);
+      if constexpr (AHEAD) {
+        if (j + kAhead < kTiles) v_ahead[j % kAhead] = v(j + kAhead);
+      }
 #pragma unroll
       for (int i = 0; i < NQ; ++i) o[i][j] = mfma_pv(op, p16[i][j / kPer], o[i][j]);
+      if constexpr (AHEAD) __builtin_amdgcn_sched_barrier(0);
     }
   }
 
@@ -707,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, tokens_per_cu(D)) kv4_tokens(Kv4Atte
     auto ks = [&](int s, int g) { return *reinterpret_cast<const f4*>(&shared.s[wave][g][16 * s + 4 * kb]); };
     auto vs = [&](int s, int g) { return *reinterpret_cast<const f4*>(&shared.s[wave][g][32 + 16 * s + 4 * kb]); };
     auto there = [&](int s) { return s ? pages[1] >= 0 : pages[0] >= 0; };
-    rows.template step<BF>(token, kb, masked, k, v, ks, vs, there);
+    rows.template step<BF, false>(token, kb, masked, k, v, ks, vs, there);
   };
 
   // The pages of 32 steps, a lane each, so that no step waits for a table entry.
@@ -933,6 +953,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_rows(Kv4AttentionArgs a, Plan
   float top_ref[(kArrays + kWaves - 1) / kWaves];      // of the V scales that this wave stages
 #pragma unroll
   for (float& r : top_ref) r = 0x1p-126f;
+  bool some_s = false;                   // whether any row may see this lane's token
   int ids = 0;                           // pages of 64 sub-tiles, a lane each
   int have = 0, have_next = 0;           // which sub-tiles of a stage may be read (bits)
   auto sub_base = [&](int page, int token) {
@@ -992,7 +1013,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_rows(Kv4AttentionArgs a, Plan
 #pragma unroll
     for (int s = 1; s < kSubs; ++s) page = kb == s ? pages[s] : page;
     const int tok = token + (lane & (S - 1));
-    const bool some = page >= 0 && tok >= t.sh.begin && tok < t.sh.end;
+    some_s = page >= 0 && tok >= t.sh.begin && tok < t.sh.end;
     const int64_t ph = (int64_t)(page >= 0 ? page : 0) * hkv + t.h;
 #pragma unroll
     for (int i = 0; i < (kArrays + kWaves - 1) / kWaves; ++i) {
@@ -1001,8 +1022,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_rows(Kv4AttentionArgs a, Plan
       const int g = arr < G ? arr : arr - G;
       gbyte* from = (arr < G ? (gbyte*)a.cache.k_scale : (gbyte*)a.cache.v_scale) +
                     ((ph * G + g) * page_size + (page >= 0 ? tok & (page_size - 1) : 0)) * 4;
-      const float s = gload<float>(from);
-      raw_s[i] = some ? s : 0.0f;
+      raw_s[i] = gload<float>(from);     // (looked at in store(): not waited for here)
     }
   };
   auto store = [&](int stage) {
@@ -1024,9 +1044,10 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_rows(Kv4AttentionArgs a, Plan
     for (int i = 0; i < (kArrays + kWaves - 1) / kWaves; ++i) {
       const int arr = wave + kWaves * i;
       if (arr >= kArrays) break;
+      const float value = some_s ? raw_s[i] : 0.0f;
       float f = scale;
       if (arr >= G) {
-        float top = __builtin_fabsf(raw_s[i]);
+        float top = __builtin_fabsf(value);
         if (__any(top > top_ref[i])) {
           for (int off = 32; off >= 1; off >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, off));
           top_ref[i] = power_above(top);
@@ -1034,7 +1055,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_rows(Kv4AttentionArgs a, Plan
         f = power_inverse(top_ref[i]);
         if (lane == 0) lds_ref[buf][arr - G] = top_ref[i];
       }
-      if (lane < S) lds_s[buf][arr][lane] = raw_s[i] * f;
+      if (lane < S) lds_s[buf][arr][lane] = value * f;
     }
   };
 
@@ -1063,7 +1084,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_rows(Kv4AttentionArgs a, Plan
       auto vs = [&](int s, int g) { return *reinterpret_cast<const f4*>(&lds_s[buf][G + g][32 * half + 16 * s + 4 * kb]); };
       auto there = [&](int s) { return (bits >> s & 1) != 0; };
       const bool masked = first < see.all_lo || first + 32 > see.all_hi || bits != 3;
-      rows.template step<BF>(first, kb, masked, k, v, ks, vs, there);
+      rows.template step<BF, true>(first, kb, masked, k, v, ks, vs, there);
     }
     if (stage + 1 < stages) store(stage + 1);
     __syncthreads();
