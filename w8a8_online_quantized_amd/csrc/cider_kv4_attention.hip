@@ -83,6 +83,7 @@ __device__ __forceinline__ T gload(gbyte* p) { return *(__attribute__((address_s
 
 // The launch of kv4_rows: how rows are tiled and tokens split (the same in its join).
 struct Plan {
+  int waves;           // of a workgroup
   int rows;            // of a workgroup's tile
   int unit;            // tokens of one step of a workgroup's loop
   int parts, least;    // most workgroups per tile, fewest steps of one
@@ -914,19 +915,21 @@ __global__ void __launch_bounds__(kThreads) kv4_join_pieces(Kv4AttentionArgs a, 
 
 // ---- many rows ------------------------------------------------------------------
 
-// Tokens of a stage of kv4_rows: two stages of operands fit the LDS of one of two
-// workgroups of a CU.
-constexpr int stage_tokens(int D) { return D == 256 ? 32 : 64; }
+// Workgroups of W waves, 4 (two per CU) or 8 (one, with twice the rows and tokens
+// per stage: a wave then unpacks half as much per token).
+// Tokens of a stage: two stages of operands are 64 KB (128 KB), of D = 64 half that.
+constexpr int stage_tokens(int D, int W) { return (D == 256 ? 32 : 64) * W / 4; }
 
-template <int D, int G, bool BF>
-__global__ void __launch_bounds__(kThreads, 2) kv4_rows(Kv4AttentionArgs a, Plan plan) {
+template <int D, int G, bool BF, int W>
+__global__ void __launch_bounds__(64 * W, 2) kv4_rows(Kv4AttentionArgs a, Plan plan) {
   constexpr int NQ = row_tiles(D, G);
   using R = Rows<D, G, NQ>;
-  constexpr int S = stage_tokens(D), kSubs = S / 16, kHalves = S / 32;
+  constexpr int S = stage_tokens(D, W), kSubs = S / 16, kHalves = S / 32;
   constexpr int kSteps = R::kSteps, kTiles = R::kTiles;
   // what a wave unpacks: steps of one sub-tile of K, tiles of one half of V
-  constexpr int kKPer = kSteps * kSubs / kWaves, kVPer = kTiles * kHalves / kWaves;
+  constexpr int kKPer = kSteps * kSubs / W, kVPer = kTiles * kHalves / W;
   constexpr int kArrays = 2 * G;         // of scales: K's groups, then V's
+  constexpr int kOwn = (kArrays + W - 1) / W, kSpan = (S + 63) / 64;   // a wave's arrays, a lane's tokens
   __shared__ u4 lds_k[2][kSubs][kSteps][64];
   __shared__ u4 lds_v[2][kHalves][kTiles][64];
   __shared__ float lds_s[2][kArrays][S];
@@ -949,11 +952,11 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_rows(Kv4AttentionArgs a, Plan
   const int k_sub = wave % kSubs, k_step = wave / kSubs * kKPer;
   const int v_half = wave % kHalves, v_tile = wave / kHalves * kVPer;
   uint32_t raw_k[kKPer], raw_v[8];
-  float raw_s[(kArrays + kWaves - 1) / kWaves];
-  float top_ref[(kArrays + kWaves - 1) / kWaves];      // of the V scales that this wave stages
+  float raw_s[kOwn][kSpan];
+  float top_ref[kOwn];                   // of the V scales that this wave stages
 #pragma unroll
   for (float& r : top_ref) r = 0x1p-126f;
-  bool some_s = false;                   // whether any row may see this lane's token
+  bool some_s[kSpan];                    // whether any row may see this lane's tokens
   int ids = 0;                           // pages of 64 sub-tiles, a lane each
   int have = 0, have_next = 0;           // which sub-tiles of a stage may be read (bits)
   auto sub_base = [&](int page, int token) {
@@ -1008,21 +1011,24 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_rows(Kv4AttentionArgs a, Plan
 #pragma unroll
       for (int i = 0; i < 4; ++i) raw_v[4 * s + i] = gload<uint16_t>(v + i * (D / 2));
     }
-    // scales: a token per lane
-    int page = pages[0];
+    // scales: a token (or two, 64 apart) per lane
 #pragma unroll
-    for (int s = 1; s < kSubs; ++s) page = kb == s ? pages[s] : page;
-    const int tok = token + (lane & (S - 1));
-    some_s = page >= 0 && tok >= t.sh.begin && tok < t.sh.end;
-    const int64_t ph = (int64_t)(page >= 0 ? page : 0) * hkv + t.h;
+    for (int p = 0; p < kSpan; ++p) {
+      int page = pages[4 * p];
 #pragma unroll
-    for (int i = 0; i < (kArrays + kWaves - 1) / kWaves; ++i) {
-      const int arr = wave + kWaves * i;
-      if (arr >= kArrays) break;
-      const int g = arr < G ? arr : arr - G;
-      gbyte* from = (arr < G ? (gbyte*)a.cache.k_scale : (gbyte*)a.cache.v_scale) +
-                    ((ph * G + g) * page_size + (page >= 0 ? tok & (page_size - 1) : 0)) * 4;
-      raw_s[i] = gload<float>(from);     // (looked at in store(): not waited for here)
+      for (int s = 1; s < (kSubs < 4 ? kSubs : 4); ++s) page = kb == s ? pages[4 * p + s] : page;
+      const int tok = token + 64 * p + (lane & (S - 1) & 63);
+      some_s[p] = page >= 0 && tok >= t.sh.begin && tok < t.sh.end;
+      const int64_t ph = (int64_t)(page >= 0 ? page : 0) * hkv + t.h;
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i) {
+        const int arr = wave + W * i;
+        if (arr >= kArrays) break;
+        const int g = arr < G ? arr : arr - G;
+        gbyte* from = (arr < G ? (gbyte*)a.cache.k_scale : (gbyte*)a.cache.v_scale) +
+                      ((ph * G + g) * page_size + (page >= 0 ? tok & (page_size - 1) : 0)) * 4;
+        raw_s[i][p] = gload<float>(from);  // (looked at in store(): not waited for here)
+      }
     }
   };
   auto store = [&](int stage) {
@@ -1041,13 +1047,16 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_rows(Kv4AttentionArgs a, Plan
       for (int n = 0; n < 2; ++n) lds_v[buf][v_half][v_tile + n][lane] = v_operand(w, n, v_nib);
     }
 #pragma unroll
-    for (int i = 0; i < (kArrays + kWaves - 1) / kWaves; ++i) {
-      const int arr = wave + kWaves * i;
+    for (int i = 0; i < kOwn; ++i) {
+      const int arr = wave + W * i;
       if (arr >= kArrays) break;
-      const float value = some_s ? raw_s[i] : 0.0f;
-      float f = scale;
+      float value[kSpan], f = scale, top = 0.0f;
+#pragma unroll
+      for (int p = 0; p < kSpan; ++p) {
+        value[p] = some_s[p] ? raw_s[i][p] : 0.0f;
+        top = __builtin_fmaxf(top, __builtin_fabsf(value[p]));
+      }
       if (arr >= G) {
-        float top = __builtin_fabsf(value);
         if (__any(top > top_ref[i])) {
           for (int off = 32; off >= 1; off >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, off));
           top_ref[i] = power_above(top);
@@ -1055,7 +1064,9 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_rows(Kv4AttentionArgs a, Plan
         f = power_inverse(top_ref[i]);
         if (lane == 0) lds_ref[buf][arr - G] = top_ref[i];
       }
-      if (lane < S) lds_s[buf][arr][lane] = value * f;
+#pragma unroll
+      for (int p = 0; p < kSpan; ++p)
+        if (S >= 64 || lane < S) lds_s[buf][arr][64 * p + lane] = value[p] * f;
     }
   };
 
@@ -1129,18 +1140,38 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_rows(Kv4AttentionArgs a, Plan
 
 // ---- the join -------------------------------------------------------------------
 
-// The parts of each row, joined. One workgroup per row: D / 8 lanes hold its
-// dimensions, and the workgroup's slices take the parts in turn.
-constexpr int kMaxParts = kThreads;
+// An average in pieces: (m, l, o) each, joined in their order.
+struct Average {
+  float top = kLeast, sum = 0.0f, out[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  __device__ __forceinline__ void add(float m, float l, const f4& u, const f4& w) {
+    if (l == 0.0f) return;               // a piece without a visible token holds nothing
+    const float to = __builtin_fmaxf(top, m);
+    const float f = __builtin_amdgcn_exp2f(top - to), g = __builtin_amdgcn_exp2f(m - to) * l;
+    top = to;
+    sum = __builtin_fmaf(sum, f, g);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      out[e] = __builtin_fmaf(g, u[e], out[e] * f);
+      out[4 + e] = __builtin_fmaf(g, w[e], out[4 + e] * f);
+    }
+  }
+};
 
-template <int D, bool BF>
+// The parts of each row, joined: SLICES * D / 8 threads hold a row, the slices take
+// its parts in turn (1 where there are few parts: sixteen rows of 128 per workgroup;
+// a workgroup per row instead took 270 us for 131072 rows of two parts).
+constexpr int kMaxParts = 256;
+
+template <int D, bool BF, int SLICES>
 __global__ void __launch_bounds__(kThreads) kv4_join(Kv4AttentionArgs a, Plan plan) {
-  constexpr int kLanes = D / 8, kSlices = kThreads / kLanes;
-  __shared__ float weight[kMaxParts], wave_top[kWaves], wave_sum[kWaves];
-  __shared__ float slice_o[kSlices][D];
-  const int64_t row = blockIdx.x;
-  const int64_t token = row / a.q_heads;
-  const int head = (int)(row - token * a.q_heads), heads = a.q_heads / a.cache.kv_heads;
+  constexpr int kLanes = D / 8, kRows = kThreads / (kLanes * SLICES);
+  __shared__ float slice_o[SLICES > 1 ? SLICES : 1][SLICES > 1 ? D : 1], slice_ml[SLICES > 1 ? SLICES : 1][2];
+  static_assert(SLICES == 1 || kRows == 1);
+  const int row = blockIdx.x * kRows + threadIdx.x / (kLanes * SLICES);
+  const int c = threadIdx.x % kLanes, slice = threadIdx.x / kLanes % SLICES;
+  if (row >= (int)a.T * a.q_heads) return;
+  const int token = row / a.q_heads;
+  const int head = row - token * a.q_heads, heads = a.q_heads / a.cache.kv_heads;
   int64_t b;
   if (a.query_offsets) {
     int64_t lo = 0, hi = a.B;           // the last sequence that begins at or before the token
@@ -1150,90 +1181,73 @@ __global__ void __launch_bounds__(kThreads) kv4_join(Kv4AttentionArgs a, Plan pl
     }
     b = lo;
   } else {
-    b = token / (a.T / a.B);
+    b = token / (int)(a.T / a.B);
   }
   const Sequence seq = sequence(a, b);
   const int64_t tok = token - seq.q0;
   if (tok < 0 || tok >= seq.n) return;
   const int rows = seq.n * heads;
-  const int row0 = (int)((tok * heads + head % heads) / plan.rows) * plan.rows;
+  const int row0 = ((int)tok * heads + head % heads) / plan.rows * plan.rows;
   const int last = min(rows, row0 + plan.rows) - 1;
   const Share sh = share(a, plan, seq, row0 / heads, last / heads);
   if (sh.parts == 1) return;            // written by its workgroup
-  const int c = threadIdx.x % kLanes, slice = threadIdx.x / kLanes, wave = threadIdx.x >> 6;
-
-  float m = kLeast, l = 0.0f;
-  if ((int)threadIdx.x < sh.parts) {
-    const float2 ml = *part_ml(a, plan, threadIdx.x, row, D);
-    m = ml.x;
-    l = ml.y;
-  }
-  float top = m;
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, off));
-  if ((threadIdx.x & 63) == 0) wave_top[wave] = top;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) top = __builtin_fmaxf(top, wave_top[w]);
-  const float f = __builtin_amdgcn_exp2f(m - top) * l;
-  float sum = f;
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off);
-  if ((threadIdx.x & 63) == 0) wave_sum[wave] = sum;
-  weight[threadIdx.x] = f;
-  __syncthreads();
-  sum = 0.0f;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) sum += wave_sum[w];
-
-  float out[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) out[e] = 0.0f;
+  Average avg;
 #pragma unroll 2
-  for (int p = slice; p < sh.parts; p += kSlices) {
+  for (int p = slice; p < sh.parts; p += SLICES) {
+    const float2 ml = *part_ml(a, plan, p, row, D);
     const float* po = part_row(a, p, row, D) + 8 * c;
-    const f4 u = *reinterpret_cast<const f4*>(po), w = *reinterpret_cast<const f4*>(po + 4);
-    const float g = weight[p];
-    if (g != 0.0f) {                    // a part without a visible token holds nothing
+    avg.add(ml.x, ml.y, *reinterpret_cast<const f4*>(po), *reinterpret_cast<const f4*>(po + 4));
+  }
+  if constexpr (SLICES > 1) {
+    if (slice > 0) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        out[e] = __builtin_fmaf(g, u[e], out[e]);
-        out[4 + e] = __builtin_fmaf(g, w[e], out[4 + e]);
+      for (int e = 0; e < 8; ++e) slice_o[slice][8 * c + e] = avg.out[e];
+      if (c == 0) {
+        slice_ml[slice][0] = avg.top;
+        slice_ml[slice][1] = avg.sum;
       }
     }
-  }
-  const int used = min(kSlices, sh.parts);
-  if (slice > 0 && slice < used) {
+    __syncthreads();
+    if (slice > 0) return;
+    for (int s = 1; s < min(SLICES, sh.parts); ++s) {
+      // (a slice's sums are not averages yet: their weight is l / l)
+      const float to = __builtin_fmaxf(avg.top, slice_ml[s][0]);
+      const float f = __builtin_amdgcn_exp2f(avg.top - to), g = __builtin_amdgcn_exp2f(slice_ml[s][0] - to);
+      avg.top = to;
+      avg.sum = avg.sum * f + slice_ml[s][1] * g;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) slice_o[slice][8 * c + e] = out[e];
+      for (int e = 0; e < 8; ++e) avg.out[e] = avg.out[e] * f + slice_o[s][8 * c + e] * g;
+    }
   }
-  __syncthreads();
-  if (slice > 0) return;
-  for (int s = 1; s < used; ++s) {
+  const float inv = avg.sum == 0.0f ? 0.0f : 1.0f / avg.sum;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) out[e] += slice_o[s][8 * c + e];
-  }
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) out[e] *= inv;
-  store16(static_cast<uint16_t*>(a.y) + row * D, c, pack8<BF>(out));
+  for (int e = 0; e < 8; ++e) avg.out[e] *= inv;
+  store16(static_cast<uint16_t*>(a.y) + (int64_t)row * D, c, pack8<BF>(avg.out));
 }
 
 // ---- the launch -------------------------------------------------------------------
 
 bool few_rows(int64_t T, int64_t B, int heads) { return T * heads <= 32 * B; }
 
+// kv4_rows. Eight waves per workgroup from 8192 rows per sequence and key/value head
+// on (one prompt of 8192 tokens, two query heads each: 324 us, four waves 358; 4096
+// tokens 125, 130; 2048 tokens 69, 67; five of about 1000 tokens, three heads of 64: 79, 63).
+// Tokens are split so that there are as many parts as workgroups are resident, or
+// twice as many for whole prompts, whose first tiles see few tokens (a prompt of 2048
+// tokens: 1 part 119 us with its join of then, 4 parts 67; 512 queries on 32768
+// tokens: 8 parts 205, 16 parts 220).
 Plan plan_of(int64_t T, int64_t B, int q_heads, int kv_heads, int head_dim, int groups, int64_t capacity, bool ragged) {
   const int heads = q_heads / kv_heads;
   Plan p;
-  p.rows = kWaves * 16 * row_tiles(head_dim, groups);
-  p.unit = stage_tokens(head_dim);
-  p.least = 512 / p.unit;
+  p.waves = T * heads >= 8192 * B ? 8 : 4;
+  p.rows = p.waves * 16 * row_tiles(head_dim, groups);
+  p.unit = stage_tokens(head_dim, p.waves);
+  p.least = std::max(1, 256 / p.unit);
   p.tiles_per = (T / B * heads + p.rows - 1) / p.rows;
   p.slots = ragged ? T * heads / p.rows + B : B * p.tiles_per;
   const int64_t steps = (capacity + p.unit - 1) / p.unit, tiles = std::max<int64_t>(p.slots * kv_heads, 1);
-  p.parts = (int)std::max<int64_t>(1, std::min<int64_t>({(512 + tiles - 1) / tiles, (steps + p.least - 1) / p.least,
-                                                         kMaxParts}));
+  const int64_t resident = p.waves == 8 ? 256 : 512, want = capacity < 2 * (T / B) ? 2 * resident : resident;
+  p.parts = (int)std::max<int64_t>(1, std::min<int64_t>({(want + tiles / 2) / tiles, (steps + p.least - 1) / p.least, kMaxParts}));
   return p;
 }
 
@@ -1262,8 +1276,15 @@ void launch_attention_t(const Kv4AttentionArgs& a, hipStream_t st) {
     return;
   }
   const Plan p = plan_of(a.T, a.B, a.q_heads, hkv, D, G, capacity, a.query_offsets != nullptr);
-  kv4_rows<D, G, BF><<<dim3((unsigned)(p.slots * p.parts * hkv)), block, 0, st>>>(a, p);
-  if (p.parts > 1) kv4_join<D, BF><<<dim3((unsigned)(a.T * a.q_heads)), block, 0, st>>>(a, p);
+  const dim3 grid((unsigned)(p.slots * p.parts * hkv));
+  if (p.waves == 8) kv4_rows<D, G, BF, 8><<<grid, dim3(512), 0, st>>>(a, p);
+  else kv4_rows<D, G, BF, 4><<<grid, block, 0, st>>>(a, p);
+  if (p.parts > 8) {
+    kv4_join<D, BF, kThreads / (D / 8)><<<dim3((unsigned)(a.T * a.q_heads)), block, 0, st>>>(a, p);
+  } else if (p.parts > 1) {
+    constexpr int kRows = kThreads / (D / 8);
+    kv4_join<D, BF, 1><<<dim3((unsigned)((a.T * a.q_heads + kRows - 1) / kRows)), block, 0, st>>>(a, p);
+  }
 }
 
 template <bool BF>
@@ -1290,7 +1311,7 @@ bool kv4_attention_fits(int64_t T, int64_t B, int q_heads, int kv_heads, int hea
   }
   for (int i = 0; i < 6; ++i) {
     const Plan p = plan_of(T, B, q_heads, kv_heads, head_dim, 1 << i / 2, capacity, i % 2);
-    if (p.slots * p.parts * kv_heads * kThreads >= kLimit) return false;
+    if (p.slots * p.parts * kv_heads * 64 * p.waves >= kLimit) return false;
     if (p.parts > 1 && T * q_heads * kThreads >= kLimit) return false;
   }
   return true;
