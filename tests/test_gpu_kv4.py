@@ -220,6 +220,30 @@ def test_append_values_at_the_borders(D, gs, dtype):
         assert torch.equal(scale.isnan(), hit) and torch.equal(scale[~hit], s[~hit])
 
 
+@pytest.mark.parametrize("dtype,interleaved", [("fp16", False), ("bf16", True)])
+def test_results_past_the_cache(dtype, interleaved):
+    """Results of 64 MB and more are stored another way: the same values as in parts."""
+    c, t, g = cider(), DT[dtype], gen(6)
+    T, Hq, Hkv, D = 9000, 32, 16, 128
+    q, k, v = rnd(g, T, Hq, D, t=t), rnd(g, T, Hkv, D, t=t), rnd(g, T, Hkv, D, t=t)
+    assert 2 * q.numel() >= 64 << 20 and 4 * k.numel() >= 64 << 20
+    freq, _ = c.rope_frequencies(D)
+    pos, slots = torch.arange(T, device="cuda").to(torch.int32), torch.arange(T, device="cuda").to(torch.int32)
+    kw = dict(inv_freq=freq, interleaved=interleaved)
+    y = c.cider_rope(q, pos, **kw)
+    whole, parts = c.kv4_cache(71, Hkv, 128, D, 64), c.kv4_cache(71, Hkv, 128, D, 64)
+    out = c.cider_kv4_append(whole, k, v, slots, q=q, positions=pos, **kw)
+    rows = c.cider_kv4_read(whole, slots, out_dtype=t)
+    for lo in range(0, T, 3000):
+        at = slice(lo, lo + 3000)
+        p, s = pos[at].clone(), slots[at].clone()
+        assert torch.equal(c.cider_rope(q[at], p, **kw), y[at])
+        assert torch.equal(c.cider_kv4_append(parts, k[at], v[at], s, q=q[at], positions=p, **kw), out[at])
+        for a, b in zip(c.cider_kv4_read(whole, s, out_dtype=t), rows):
+            assert torch.equal(a, b[at])
+    assert all(torch.equal(a, b) for a, b in zip(whole, parts)) and torch.equal(out, y)
+
+
 # ---- attention --------------------------------------------------------------
 
 def filled(g, c, pages, Hkv, page, D, gs, t):

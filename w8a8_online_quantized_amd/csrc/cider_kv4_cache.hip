@@ -98,7 +98,7 @@ __device__ __forceinline__ uint32_t nibbles_of_values(const float (&x)[8], float
 // A wave has one token, or a slice of its heads: its lanes first form the cosines
 // and sines, and each keeps those of its eight dimensions. Then 64 / LANES heads of
 // q, of k or of v at a time, the next ones on their way while some are worked on.
-template <int LANES, bool BF>
+template <int LANES, bool BF, bool PAST>
 __global__ void __launch_bounds__(kThreads) kv4_append_rows(Kv4AppendArgs a) {
   constexpr int D = LANES * 8, kHeads = 64 / LANES;
   __shared__ float2 turns[kThreads / 64][D / 2];
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kThreads) kv4_append_rows(Kv4AppendArgs a) {
       const int head = i * kHeads + lane / LANES;
       const u4 y = turned(x, a.q_norm != nullptr, q_norm);
       if (head < a.q_heads)
-        store16(static_cast<uint16_t*>(a.q_out) + t * a.out_row_stride + head * a.out_head_stride, c, y);
+        store16_to<PAST>(static_cast<uint16_t*>(a.q_out) + t * a.out_row_stride + head * a.out_head_stride, c, y);
       continue;
     }
     if (!stored) continue;
@@ -257,7 +257,7 @@ __device__ __forceinline__ float code_value(uint32_t nibble, float s) {
 }
 
 // A thread's next row is on its way while one is written.
-template <int LANES, bool BF>
+template <int LANES, bool BF, bool PAST>
 __global__ void __launch_bounds__(kThreads) kv4_read_rows(Kv4Cache cache, const int32_t* __restrict__ slots, int64_t n,
                                                           uint16_t* __restrict__ k, uint16_t* __restrict__ v) {
   constexpr int D = LANES * 8, kHeads = kThreads / LANES;
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kThreads) kv4_read_rows(Kv4Cache cache, const 
     float t[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) t[e] = cur.there ? code_value((cur.codes >> (4 * e)) & 15u, cur.s) : 0.0f;
-    store16((cur.is_v ? v : k) + cur.to * D, c, pack8<BF>(t));
+    store16_to<PAST>((cur.is_v ? v : k) + cur.to * D, c, pack8<BF>(t));
     cur = next;
   }
 }
@@ -321,15 +321,21 @@ void launch_append_t(const Kv4AppendArgs& a, hipStream_t st) {
   const int steps = (a.q_heads + kHeads - 1) / kHeads + 2 * ((a.cache.kv_heads + kHeads - 1) / kHeads);
   // slices of a token's heads until there are waves for the whole GPU
   const int64_t slices = std::min<int64_t>(steps, std::max<int64_t>(1, 4096 / a.T));
-  kv4_append_rows<LANES, BF><<<dim3((unsigned)((a.T + kTok - 1) / kTok), (unsigned)slices), dim3(kThreads), 0, st>>>(a);
+  const dim3 grid((unsigned)((a.T + kTok - 1) / kTok), (unsigned)slices), block(kThreads);
+  if (2 * a.T * a.q_heads * a.cache.head_dim >= kPastCacheBytes) kv4_append_rows<LANES, BF, true><<<grid, block, 0, st>>>(a);
+  else kv4_append_rows<LANES, BF, false><<<grid, block, 0, st>>>(a);
 }
 
 template <int LANES, bool BF>
 void launch_read_t(const Kv4Cache& cache, const int32_t* slots, int64_t n, void* k, void* v, hipStream_t st) {
   constexpr int kHeads = kThreads / LANES;
   const int64_t blocks = (n * 2 * cache.kv_heads + kHeads - 1) / kHeads;
-  kv4_read_rows<LANES, BF><<<dim3((unsigned)(blocks < 2048 ? blocks : 2048)), dim3(kThreads), 0, st>>>(
-      cache, slots, n, static_cast<uint16_t*>(k), static_cast<uint16_t*>(v));
+  const dim3 grid((unsigned)std::min<int64_t>(blocks, 2048)), block(kThreads);
+  uint16_t *to_k = static_cast<uint16_t*>(k), *to_v = static_cast<uint16_t*>(v);
+  if (4 * n * cache.kv_heads * cache.head_dim >= kPastCacheBytes)
+    kv4_read_rows<LANES, BF, true><<<grid, block, 0, st>>>(cache, slots, n, to_k, to_v);
+  else
+    kv4_read_rows<LANES, BF, false><<<grid, block, 0, st>>>(cache, slots, n, to_k, to_v);
 }
 
 }  // namespace

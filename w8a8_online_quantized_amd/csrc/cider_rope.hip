@@ -19,7 +19,7 @@ constexpr int kThreads = 256;
 //   half layout, 16-byte chunks: pair of chunks (c, c + rd / 16), c < rd / 16;
 //       then the chunks behind rd, one each
 //   interleaved: one chunk of 8 (4 pairs, or fewer at rd's end, or none)
-template <bool BF, bool INTERLEAVED>
+template <bool BF, bool INTERLEAVED, bool PAST>
 __global__ void __launch_bounds__(kThreads) rope_rows(RopeArgs a) {
   __shared__ float2 turn[kMaxRotaryPairs];
   const int64_t t = blockIdx.x;
@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(kThreads) rope_rows(RopeArgs a) {
         const int i = 4 * c + e;
         if (i < pairs) rope_pair(v[2 * e], v[2 * e + 1], turn[i]);
       }
-      store16(yh, c, pack8<BF>(v));
+      store16_to<PAST>(yh, c, pack8<BF>(v));
     } else {
       const int step = pairs / 8;
       if (c < step) {
@@ -52,10 +52,10 @@ __global__ void __launch_bounds__(kThreads) rope_rows(RopeArgs a) {
         unpack8<BF>(load16(xh, c + step), w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) rope_pair(u[e], w[e], turn[8 * c + e]);
-        store16(yh, c, pack8<BF>(u));
-        store16(yh, c + step, pack8<BF>(w));
+        store16_to<PAST>(yh, c, pack8<BF>(u));
+        store16_to<PAST>(yh, c + step, pack8<BF>(w));
       } else {
-        store16(yh, c + step, load16(xh, c + step));
+        store16_to<PAST>(yh, c + step, load16(xh, c + step));
       }
     }
   }
@@ -103,12 +103,18 @@ int64_t slices(const RopeArgs& a) {
   return ((int64_t)a.heads * per_head + kThreads - 1) / kThreads;
 }
 
+template <bool BF, bool PAST>
+void launch_rope_rows(const RopeArgs& a, dim3 grid, hipStream_t st) {
+  if (a.interleaved) rope_rows<BF, true, PAST><<<grid, dim3(kThreads), 0, st>>>(a);
+  else rope_rows<BF, false, PAST><<<grid, dim3(kThreads), 0, st>>>(a);
+}
+
 template <bool BF>
 hipError_t launch_rope_t(const RopeArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)a.T, (unsigned)slices(a)), block(kThreads);
-  if (!whole_chunks(a)) rope_elements<BF><<<grid, block, 0, st>>>(a);
-  else if (a.interleaved) rope_rows<BF, true><<<grid, block, 0, st>>>(a);
-  else rope_rows<BF, false><<<grid, block, 0, st>>>(a);
+  const dim3 grid((unsigned)a.T, (unsigned)slices(a));
+  if (!whole_chunks(a)) rope_elements<BF><<<grid, dim3(kThreads), 0, st>>>(a);
+  else if (2 * a.T * a.heads * a.head_dim >= kPastCacheBytes) launch_rope_rows<BF, true>(a, grid, st);
+  else launch_rope_rows<BF, false>(a, grid, st);
   return hipGetLastError();
 }
 
