@@ -514,10 +514,10 @@ struct Raw {
   float s[G];
 };
 
-// Steps of kv4_tokens in registers, and workgroups that a CU then holds at once.
-// (D = 256 needs more than 256 registers: one wave per SIMD 35.5 us for 24 requests
-// of 5 queries in a window of 3000, two with spills 54.7).
-constexpr int ring_steps(int D) { return D == 256 ? 2 : 3; }
+// Workgroups of kv4_tokens that a CU holds at once: two waves per SIMD, without
+// spills (three: the decode batch below 117 us instead of 86), one for D = 256, which
+// needs more than 256 registers (24 requests of 5 queries in a window of 3000: two 55
+// us with spills, one 35).
 constexpr int tokens_per_cu(int D) { return D == 256 ? 1 : 2; }
 
 template <int D, int G, bool BF>
@@ -741,10 +741,11 @@ __global__ void __launch_bounds__(kThreads, tokens_per_cu(D)) kv4_tokens(Kv4Atte
     int token, pages[2];
     Raw<D, G> raw;
   };
-  // kRing steps in registers: the others on their way while one is worked on. The
-  // loads are unconditional (past the end, of the last codes again): behind a branch
-  // the wait for one step's would be one for all in flight.
-  constexpr int kRing = ring_steps(D);
+  // Two steps in registers, one on its way while the other is worked on (64 requests
+  // of up to 8192 tokens 86 us; three steps 90, four 92). The loads are unconditional
+  // (past the end, of the last codes again): behind a branch the wait for one step's
+  // would be one for all in flight.
+  constexpr int kRing = 2;
   Step ring[kRing];
   auto fetch = [&](Step& to) {
     if (at == 64) {
@@ -1229,24 +1230,29 @@ __global__ void __launch_bounds__(kThreads) kv4_join(Kv4AttentionArgs a, Plan pl
 
 bool few_rows(int64_t T, int64_t B, int heads) { return T * heads <= 32 * B; }
 
-// kv4_rows. Eight waves per workgroup from 8192 rows per sequence and key/value head
-// on (one prompt of 8192 tokens, two query heads each: 324 us, four waves 358; 4096
-// tokens 125, 130; 2048 tokens 69, 67; five of about 1000 tokens, three heads of 64: 79, 63).
-// Tokens are split so that there are as many parts as workgroups are resident, or
-// twice as many for whole prompts, whose first tiles see few tokens (a prompt of 2048
-// tokens: 1 part 119 us with its join of then, 4 parts 67; 512 queries on 32768
-// tokens: 8 parts 205, 16 parts 220).
+// kv4_rows. Whole prompts (no more than twice as many tokens as queries) have tiles of
+// all lengths, which are done as workgroups come free; other queries see about as many
+// tokens each. Eight waves per workgroup pay from 8192 rows per sequence and key/value
+// head in the first case (heads of 128, two query heads each; us with 8, 4 waves: 8192
+// tokens 324, 358; 4096 tokens 122, 124; 2048 tokens 69, 67; five of about 1000 tokens,
+// three heads of 64: 81, 65), from 1024 in the second (512 queries on 8192 tokens 68, 71;
+// on 32768 175, 190). Tokens are split until there are as many parts as workgroups are
+// resident, for whole prompts twice as many (2048 tokens: 2 parts 119, 4 parts 67; 512
+// queries on 32768 tokens: 8 parts 190, 16 parts 220).
 Plan plan_of(int64_t T, int64_t B, int q_heads, int kv_heads, int head_dim, int groups, int64_t capacity, bool ragged) {
   const int heads = q_heads / kv_heads;
+  const int64_t rows = T * heads;
+  const bool prompts = capacity < 2 * (T / B);
   Plan p;
-  p.waves = T * heads >= 8192 * B ? 8 : 4;
+  p.waves = rows >= (prompts ? 8192 : 1024) * B ? 8 : 4;
   p.rows = p.waves * 16 * row_tiles(head_dim, groups);
   p.unit = stage_tokens(head_dim, p.waves);
   p.least = std::max(1, 256 / p.unit);
   p.tiles_per = (T / B * heads + p.rows - 1) / p.rows;
-  p.slots = ragged ? T * heads / p.rows + B : B * p.tiles_per;
-  const int64_t steps = (capacity + p.unit - 1) / p.unit, tiles = std::max<int64_t>(p.slots * kv_heads, 1);
-  const int64_t resident = p.waves == 8 ? 256 : 512, want = capacity < 2 * (T / B) ? 2 * resident : resident;
+  p.slots = ragged ? rows / p.rows + B : B * p.tiles_per;
+  const int64_t steps = (capacity + p.unit - 1) / p.unit, resident = p.waves == 8 ? 256 : 512;
+  const int64_t want = prompts ? 2 * resident : resident;
+  const int64_t tiles = B * ((rows + B * p.rows - 1) / (B * p.rows)) * kv_heads;   // of sequences of one length
   p.parts = (int)std::max<int64_t>(1, std::min<int64_t>({(want + tiles / 2) / tiles, (steps + p.least - 1) / p.least, kMaxParts}));
   return p;
 }
