@@ -695,13 +695,16 @@ cider_status_t cider_kv4_read(const cider_kv4_cache_t* cache, const int32_t* slo
  *   window     : 0, or the tokens j > p - window only.
  * A row that sees no token is zeros. Scores and the softmax's sums are fp32;
  * the weights are rounded to fp16 (11 bits) once they are multiplied by V's
- * scale. exp2 is the GPU's fp32 instruction.
+ * scale, in units of a power of two above the largest finite scale of V (of
+ * that group of dimensions) that rows of the sequence see: what is below 2^-25
+ * of that scale is nothing. exp2 is the GPU's fp32 instruction.
  * workspace: 16-byte aligned, at least cider_kv4_attention_workspace_size bytes
  * (capacity = max_pages * page_size; 0: none, NULL then). Its contents are
- * scratch; calls that share one must not overlap in time. The result depends
- * on T, B and the capacity through the order of its sums, and on nothing else
- * but the inputs. T * q_heads < 2^31, B >= 1, capacity < 2^31, softmax_scale finite;
- * sizes whose grid would take 2^31 GPU threads return
+ * scratch; calls that share one must not overlap in time. The order of a row's
+ * sums depends on T, B, the capacity and the lengths of all sequences, so a
+ * sequence alone and in a batch may differ by roundings; the same call gives
+ * the same bits. T * q_heads <= 2^30, B >= 1, capacity <= 2^30, softmax_scale
+ * finite; sizes whose grid would take 2^31 GPU threads return
  * CIDER_ERROR_INVALID_VALUE. */
 typedef struct {
   cider_kv4_cache_t cache;

@@ -120,7 +120,8 @@ def attend_args(cache_kw=None, **kw):
     dict(softmax_scale=float("nan")), dict(softmax_scale=float("inf")), dict(q=None), dict(y=None), dict(lengths=None),
     dict(page_table=None), dict(q=PTR + 8), dict(y=PTR + 8), dict(lengths=PTR + 4), dict(page_table=PTR + 4),
     dict(query_offsets=PTR + 4), dict(workspace=PTR + 4), dict(workspace=None), dict(workspace_bytes=16),
-    dict(q_row_stride=-8), dict(q_row_stride=516), dict(q_head_stride=100), dict(T=1 << 30, B=1 << 30)])
+    dict(q_row_stride=-8), dict(q_row_stride=516), dict(q_head_stride=100), dict(T=1 << 30, B=1 << 30),
+    dict(max_pages=(1 << 26) + 1)])
 def test_attention_rejects(L, bad):
     assert L.cider_kv4_attention(ctypes.byref(attend_args(**bad)), NULL) == INV
 
@@ -147,7 +148,7 @@ def test_attention_workspace_query(L):
     assert many > 0 and many % (512 * 16 * 130 * 4) == 0
     for bad in ((-1, 1, 16, 8, 128, 64), (1, 0, 16, 8, 128, 64), (1, 1, 15, 8, 128, 64), (1, 1, 16, 0, 128, 64),
                 (1, 1, 16, 8, 96, 64), (1, 1, 16, 8, 128, -1), (1, 1, 16, 8, 128, 1 << 31), (1 << 31, 1, 16, 8, 128, 64),
-                (1 << 28, 1, 16, 8, 128, 64)):
+                (1 << 28, 1, 16, 8, 128, 64), (1, 1, 16, 8, 128, (1 << 30) + 16), ((1 << 26) + 1, 1 << 26, 16, 8, 128, 64)):
         assert q(*bad) == -1, bad
     with pytest.raises(ValueError):
         cider.cider_kv4_attention_workspace_size(1, 1, 16, (1 << 32) + 8, 128, 64)

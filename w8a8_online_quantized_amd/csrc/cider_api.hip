@@ -818,12 +818,13 @@ cider_status_t cider_kv4_read(const cider_kv4_cache_t* cache, const int32_t* slo
 
 static bool kv4_attention_sizes_ok(int64_t T, int64_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                                    int64_t capacity) {
-  constexpr int64_t kLimit = int64_t(1) << 31;
-  if (T < 0 || T >= kLimit || B < 1 || B >= kLimit || capacity < 0 || capacity >= kLimit || kv_heads < 1 ||
+  // (tokens and positions are int32 with some steps of a loop past them, window and queries before them)
+  constexpr int64_t kLimit = int64_t(1) << 31, kMost = int64_t(1) << 30;
+  if (T < 0 || T > kMost || B < 1 || B >= kLimit || capacity < 0 || capacity > kMost || kv_heads < 1 ||
       kv_heads > CIDER_KV4_MAX_HEADS || q_heads < 1 || q_heads > CIDER_KV4_MAX_Q_HEADS || q_heads % kv_heads)
     return false;
   if (head_dim != 64 && head_dim != 128 && head_dim != 256) return false;
-  return T == 0 || (T * q_heads < kLimit && cider::kv4_attention_fits(T, B, q_heads, kv_heads, head_dim, capacity));
+  return T == 0 || (T * q_heads <= kMost && cider::kv4_attention_fits(T, B, q_heads, kv_heads, head_dim, capacity));
 }
 
 int64_t cider_kv4_attention_workspace_size(int64_t T, int64_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
