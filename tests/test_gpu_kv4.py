@@ -380,6 +380,43 @@ def test_nothing_hidden_is_used(n, Hq, dtype):
         check(got, q, cache, table, lens, ends, window=window)
 
 
+@pytest.mark.parametrize("D,gs", GROUPS)
+def test_nothing_hidden_is_used_of_small_pages(D, gs):
+    """Windows that begin inside a page of 16, with infinite scales before them."""
+    c, g = cider(), gen(D + gs)
+    for n, window in ((3, 9), (90, 21), (90, 40)):
+        lens, ends = [333, 500], [0, n, 2 * n]
+        q, cache, table, _ = setup(c, g, lens, [n, n], 4, 2, D, gs, 16, torch.float16)
+        wild = [a.clone() for a in cache]
+        for b, L in enumerate(lens):
+            for at in range(L - n - window + 1):
+                for side in (1, 3):
+                    wild[side][int(table[b, at // 16]), :, :, at % 16] = float("inf") if at % 2 else 1e30
+        got = c.cider_kv4_attention(q, c.KV4Cache(*wild), table, i32(lens), window=window)
+        assert torch.equal(got, c.cider_kv4_attention(q, cache, table, i32(lens), window=window))
+        check(got, q, cache, table, lens, ends, window=window)
+
+
+@pytest.mark.parametrize("n", [3, 90, 1500])
+@pytest.mark.parametrize("side", [1, 3])
+def test_an_infinite_scale_reaches_only_rows_that_see_it(n, side):
+    """The rows before it, in the same tile too, are as without it (a maximum may be raised at another step); those behind
+    an infinite scale of V are not finite."""
+    c, g = cider(), gen(n)
+    lens = [n + 40, 200 + n]
+    q, cache, table, ends = setup(c, g, lens, [n] * 2, 4, 2, 128, 64, 16, torch.bfloat16)
+    want, bound, _ = ref.attention(q, cache, table, lens, ends, True, 0, 128 ** -0.5)
+    at = lens[1] - n // 2 - 1
+    wild = [a.clone() for a in cache]
+    wild[side][int(table[1, at // 16]), 1, 0, at % 16] = float("inf")
+    y = c.cider_kv4_attention(q, c.KV4Cache(*wild), table, i32(lens))
+    hit = torch.zeros_like(y, dtype=torch.bool)
+    hit[ends[1] + at - (lens[1] - n):, 2:, : 128 if side == 1 else 64] = True
+    within(y[~hit], want[~hit], bound[~hit])
+    if side == 3:
+        assert not bool(y[hit].isfinite().any())
+
+
 @pytest.mark.parametrize("n", [1, 90])
 def test_a_bad_token_reaches_only_rows_that_see_it(n):
     """A NaN scale of K or V at one token: rows that see it are NaN, the others have the bits they had."""
@@ -467,6 +504,45 @@ def test_attention_long_and_many(B, Hq, Hkv, D, n, L):
     offsets = None if n == 1 else i32(ends)
     y = c.cider_kv4_attention(q, cache, table, i32(lens), query_offsets=offsets)
     check(y, q, cache, table, lens, ends)
+
+
+# lengths, queries of each sequence, query heads, key/value heads, page size, causal, window
+LARGE = [
+    ([1100, 3000], [1100, 1024], 8, 1, 64, True, 0),             # more than 8192 rows of a key/value head, no whole prompts
+    ([6000], [1030], 2, 2, 16, True, 0),                         # from 1024 rows on a long cache: parts to join
+    ([6000, 100, 0, 4000], [2050, 100, 0, 1025], 2, 1, 32, True, 900),
+    ([2500], [1100], 1, 1, 128, False, 333),
+    ([40000], [40], 1, 1, 1024, True, 0),                        # more than eight parts
+    ([8300], [8300], 1, 1, 64, True, 0),                         # a whole prompt
+]
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("D,gs", GROUPS)
+@pytest.mark.parametrize("lens,counts,Hq,Hkv,page,causal,window", LARGE)
+def test_attention_large_tiles(lens, counts, Hq, Hkv, page, causal, window, D, gs, dtype):
+    c, g = cider(), gen(sum(lens) + D + gs)
+    q, cache, table, ends = setup(c, g, lens, counts, Hq, Hkv, D, gs, page, DT[dtype])
+    y = c.cider_kv4_attention(q, cache, table, i32(lens), query_offsets=i32(ends), causal=causal, window=window)
+    check(y, q, cache, table, lens, ends, causal, window)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("D,gs", GROUPS)
+@pytest.mark.parametrize("B,L,window", [(9, 5000, 0), (70, 900, 0), (70, 900, 200), (300, 400, 0), (3, 9000, 3000)])
+def test_attention_shares_of_a_ragged_batch(B, L, window, D, gs, dtype):
+    """Few rows of sequences of all lengths: workgroups end one, have some of their own and begin another; sequences
+    without queries or tokens between them."""
+    c, g = cider(), gen(B + L + D)
+    lens = [0 if b % 11 == 5 else 1 + (b * 7919 + 13 * b * b) % L for b in range(B)]
+    lens[B // 2] = L
+    counts = [0 if b % 7 == 3 else 1 + b % 3 for b in range(B)]
+    q, cache, table, ends = setup(c, g, lens, counts, 6, 2, D, gs, 32, DT[dtype])
+    y = torch.full((ends[-1] + 2, 6, D), 5.0, dtype=DT[dtype], device="cuda")
+    qq = torch.cat((q, q[:2]))
+    c.cider_kv4_attention(qq, cache, table, i32(lens), query_offsets=i32(ends), window=window, y=y)
+    assert bool((y[ends[-1]:] == 5).all())
+    check(y[:ends[-1]], q, cache, table, lens, ends, window=window)
 
 
 def test_a_cache_past_32_bits():

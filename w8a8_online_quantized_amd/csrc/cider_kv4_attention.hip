@@ -253,6 +253,13 @@ __device__ __forceinline__ float power_inverse(float v) {
   return __builtin_bit_cast(float, 0x7F000000u - __builtin_bit_cast(uint32_t, v));
 }
 
+// What a scale of V asks of the unit: infinities and NaN nothing, as rows that do
+// not see them share it.
+__device__ __forceinline__ float unit_size(float v) {
+  v = __builtin_fabsf(v);
+  return v < __builtin_inff() ? v : 0.0f;
+}
+
 // ---- the rows of a wave -----------------------------------------------------------
 
 template <int D, int G, int NQ>
@@ -709,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, tokens_per_cu(D)) kv4_tokens(Kv4Atte
     }
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      const float v = lane < 32 ? 0.0f : __builtin_fabsf(r.s[g]);
+      const float v = lane < 32 ? 0.0f : unit_size(r.s[g]);
       if (__any(v > rows.ref[g])) {
         float top = v;
         for (int off = 16; off >= 1; off >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, off));
@@ -1017,7 +1024,7 @@ __global__ void __launch_bounds__(64 * W, 2) kv4_rows(Kv4AttentionArgs a, Plan p
     for (int p = 0; p < kSpan; ++p) {
       int page = pages[4 * p];
 #pragma unroll
-      for (int s = 1; s < (kSubs < 4 ? kSubs : 4); ++s) page = kb == s ? pages[4 * p + s] : page;
+      for (int s = 1; s < (kSubs < 4 ? kSubs : 4); ++s) page = (lane & (S - 1) & 63) >> 4 == s ? pages[4 * p + s] : page;
       const int tok = token + 64 * p + (lane & (S - 1) & 63);
       some_s[p] = page >= 0 && tok >= t.sh.begin && tok < t.sh.end;
       const int64_t ph = (int64_t)(page >= 0 ? page : 0) * hkv + t.h;
@@ -1055,7 +1062,7 @@ __global__ void __launch_bounds__(64 * W, 2) kv4_rows(Kv4AttentionArgs a, Plan p
 #pragma unroll
       for (int p = 0; p < kSpan; ++p) {
         value[p] = some_s[p] ? raw_s[i][p] : 0.0f;
-        top = __builtin_fmaxf(top, __builtin_fabsf(value[p]));
+        top = __builtin_fmaxf(top, unit_size(value[p]));
       }
       if (arr >= G) {
         if (__any(top > top_ref[i])) {
@@ -1228,6 +1235,10 @@ __global__ void __launch_bounds__(kThreads) kv4_join(Kv4AttentionArgs a, Plan pl
 
 // ---- the launch -------------------------------------------------------------------
 
+// Up to two tiles of 16 rows per sequence and key/value head. With a threshold of 16,
+// 32 and 64 (us, 8192 tokens, heads of 128, 8 per key/value head, 2 of those): sixteen
+// sequences of 24 rows 35, 31, 31; two of 64 rows 23, 23, 30; sixteen of 64 rows 44,
+// 44, 39. Past 32 it depends on how many sequences there are, and few would lose more.
 bool few_rows(int64_t T, int64_t B, int heads) { return T * heads <= 32 * B; }
 
 // kv4_rows. Whole prompts (no more than twice as many tokens as queries) have tiles of
