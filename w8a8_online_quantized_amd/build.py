@@ -8,6 +8,8 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,7 +20,7 @@ SOURCES = ["cider_api.hip", "cider_quant.hip", "cider_gemm.hip", "cider_mv.hip",
            "cider_kv4_attention.hip"]
 
 HIPCC_FLAGS = [
-    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
+    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
     # packed fp32 VALU instructions stay off for every kernel of this library
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall", "-Wno-unused-function",
@@ -33,19 +35,36 @@ def hipcc() -> str:
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every HIP source into libcider.so; returns the library path."""
-    srcs = [os.path.join(CSRC, s) for s in SOURCES]
+    """Compile every HIP source into libcider.so; returns the library path.
+
+    The sources are compiled side by side (each is independent device code),
+    those with the most kernels first.
+    """
     tmp = LIB + ".tmp"
-    cmd = [hipcc(), *HIPCC_FLAGS, "-I", os.path.join(ROOT, "include"), *srcs, "-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    noise = "is not a recognized feature for this target"
-    msgs = "\n".join(l for l in (res.stdout + res.stderr).splitlines() if noise not in l)
-    if res.returncode != 0:
-        raise RuntimeError(f"hipcc failed ({res.returncode}):\n{msgs}")
-    if verbose and msgs.strip():
-        print(msgs)
+
+    def run(args) -> None:
+        cmd = [hipcc(), *HIPCC_FLAGS, *args]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        noise = "is not a recognized feature for this target"
+        msgs = "\n".join(l for l in (res.stdout + res.stderr).splitlines() if noise not in l)
+        if res.returncode != 0:
+            raise RuntimeError(f"hipcc failed ({res.returncode}):\n{msgs}")
+        if verbose and msgs.strip():
+            print(msgs)
+
+    with tempfile.TemporaryDirectory() as objs:
+        def compile_one(source: str) -> str:
+            obj = os.path.join(objs, source + ".o")
+            run(["-c", "-I", os.path.join(ROOT, "include"), os.path.join(CSRC, source), "-o", obj])
+            return obj
+
+        jobs = int(os.environ.get("MAX_JOBS", "") or min(8, os.cpu_count() or 1))
+        with ThreadPoolExecutor(max(1, min(jobs, 8))) as pool:
+            todo = [pool.submit(compile_one, s) for s in reversed(SOURCES)]
+            linked = [t.result() for t in todo]
+        run(["-shared", *reversed(linked), "-o", tmp])
     # every symbol of the library's own namespace must be defined in it (a
     # kernel whose host-side launch stub was not emitted links fine and only
     # fails when the library is loaded)
