@@ -1,7 +1,8 @@
 // Rotary positions of q or k rows: y = x with the first rotary_dim dimensions
 // of each head turned by its token's position (cider_rope.h).
 //
-// HBM-bound: 2 bytes in and 2 out per element. One workgroup per token (and
+// HBM-bound: 2 bytes in and 2 out per element (16384 tokens of 24 heads of 128: 201
+// MB in 39.4 us = 5.1 TB/s, a copy's rate). One workgroup per token (and
 // slice of its heads): its threads first form the token's rotary_dim / 2
 // cosines and sines into LDS, shared by all heads, while the rows' loads are on
 // their way. A thread then owns both ends of the pairs it turns, so y may be x.
