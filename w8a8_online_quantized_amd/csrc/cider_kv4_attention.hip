@@ -53,7 +53,7 @@ constexpr int kWaves = kThreads / 64;
 constexpr int kTokens = 32;            // of one step of products
 // Tiles of 16 rows of a wave of kv4_rows (W waves): what 256 registers hold without
 // spills; heads of 64 in two groups one in workgroups of four waves, of which a CU
-// then holds four (five prompts of about 1000 tokens 69 us, with two tiles 79; two
+// then holds three (five prompts of about 1000 tokens 69 us, with two tiles 79; two
 // in workgroups of eight: 512 queries on 32768 tokens 175 us, with one tile 231).
 constexpr int row_tiles(int D, int G, int W) { return D == 256 || (D / G == 32 && !(D == 64 && W == 8)) ? 1 : 2; }
 constexpr float kLog2e = 1.4426950408889634f;
@@ -937,12 +937,13 @@ __global__ void __launch_bounds__(kThreads) kv4_join_pieces(Kv4AttentionArgs a, 
 // Tokens of a stage: two stages of operands are 64 KB (128 KB), of D = 64 half that.
 constexpr int stage_tokens(int D, int W) { return (D == 256 ? 32 : 64) * W / 4; }
 
-// Waves per SIMD: two, of heads of 64 in workgroups of four waves three or four (one
-// group, five prompts of about 1000 tokens: 57 us with three, 63 with two).
-constexpr int rows_per_simd(int D, int G, int W) { return D == 64 && W == 4 ? (G == 1 ? 3 : 4) : 2; }
+// Waves per SIMD: two, of heads of 64 in workgroups of four waves three (one group,
+// five prompts of about 1000 tokens: 57 us with three, 63 with two; two groups with
+// four, which takes spills, are no faster than with three).
+constexpr int rows_per_simd(int D, int W) { return D == 64 && W == 4 ? 3 : 2; }
 
 template <int D, int G, bool BF, int W>
-__global__ void __launch_bounds__(64 * W, rows_per_simd(D, G, W)) kv4_rows(Kv4AttentionArgs a, Plan plan) {
+__global__ void __launch_bounds__(64 * W, rows_per_simd(D, W)) kv4_rows(Kv4AttentionArgs a, Plan plan) {
   constexpr int NQ = row_tiles(D, G, W);
   using R = Rows<D, G, NQ>;
   constexpr int S = stage_tokens(D, W), kSubs = S / 16, kHalves = S / 32;
