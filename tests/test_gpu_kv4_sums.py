@@ -1,0 +1,71 @@
+"""Sums of attention over long caches, to a tolerance that does not grow with the
+length: a row's error is that of the weights' fp16 rounding and of its result."""
+import pytest
+
+from tests.test_gpu_parity import cider
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+from tests import kv4_reference as ref  # noqa: E402
+from tests.test_gpu_kv4 import DT, gen, rnd  # noqa: E402
+
+U = 2.0 ** -24
+
+
+def long_cache(g, c, L, Hkv, D, G, v_mean, page=128):
+    pages = -(-L // page)
+    code = lambda mean: rnd(g, pages, Hkv, page, D, scale=2.6, mean=mean).round_().clamp_(-7, 7)  # noqa: E731
+    scale = lambda: 0.3 + 0.3 * torch.rand(pages, Hkv, G, page, generator=g, device="cuda")      # noqa: E731
+    return c.KV4Cache(ref.pack(code(0.0)), scale(), ref.pack(code(v_mean)), scale())
+
+
+def row(q, k, v, scale, sk):
+    """A row in 64 bits, the norm of independent relative errors of its weights,
+    and the size of an error of its scores."""
+    s = scale * (k @ q)
+    p = torch.softmax(s, 0)
+    # a score: D products of up to 2 * 279 |q| s_k before the offset is off, each fp32
+    # step cut (2 U), as independent errors three times the root of their number; then
+    # its scaling, the difference to the maximum and the exponential
+    score = 3 * scale * float(q.abs().sum()) * 2 * 279 * sk * U / len(q) ** 0.5 + (float(s.abs().max()) + 16) * 4 * U
+    return p @ v, (p.square() @ v.square()).sqrt(), score
+
+
+def check_rows(y, picks, q, k, v, per, scale, sk, extra=0.0):
+    """Joint error over the picked rows. Weights: half a step of fp16 each, 2^-11,
+    as independent errors (and `extra`). fp32 sums: up to 2^14 steps of a wave, each
+    cut by 2^-23, and 2^17 terms of the sum of weights, each rounded by 2^-24, as
+    independent ones 2^-16 and 2^-15.5: 2^-14. The result: half a step of its type."""
+    err = 0.0
+    weights = size = 0.0
+    for t, h in picks:
+        want, spread, score = row(q[t, h].double(), k[:, h // per], v[:, h // per], scale, sk)
+        err += float((y[t, h].double() - want).square().sum())
+        weights += float((spread * (2.0 ** -11 + extra + 2 * score)).square().sum())
+        size += float(want.square().sum())
+    allowed = weights ** 0.5 + size ** 0.5 * (torch.finfo(y.dtype).eps / 2 + 2.0 ** -14)
+    assert err ** 0.5 <= allowed, (err ** 0.5 / size ** 0.5, allowed / size ** 0.5)
+
+
+# standard deviation of q (0: every token weighs the same; 8: a few tokens have nearly all weight), mean of V's codes
+KINDS = [(0.0, 0.0), (1.0, 0.0), (8.0, 0.0), (0.0, 2.0)]
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("D,G", [(64, 1), (64, 2), (128, 1), (128, 4), (256, 2)])
+@pytest.mark.parametrize("B,n,Hq,Hkv,L", [(1, 2048, 32, 4, 131072), (64, 1, 8, 8, 131072), (1, 70, 4, 1, 131072),
+                                          (1, 1, 16, 8, 500000)])
+def test_long_sums(B, n, Hq, Hkv, L, D, G, dtype):
+    """Long ranges of one wave (many rows, and many sequences over the same pages), and parts that are joined."""
+    c, t, g = cider(), DT[dtype], gen(L + D + G + n)
+    for q_std, v_mean in KINDS:
+        cache = long_cache(g, c, L, Hkv, D, G, v_mean)
+        table = torch.arange(cache.k_codes.shape[0], device="cuda", dtype=torch.int32).repeat(B, 1)
+        q = rnd(g, B * n, Hq, D, t=t, scale=q_std)
+        y = c.cider_kv4_attention(q, cache, table, torch.full((B,), L, dtype=torch.int32, device="cuda"), causal=False)
+        k, v = ref.stored_rows(cache, torch.arange(L, device="cuda"))
+        at = torch.randint(0, B * n, (3,), generator=g, device="cuda").tolist()
+        picks = {(i, h) for i in at for h in range(0, Hq, max(1, Hq // 4))}
+        check_rows(y, picks, q, k, v, Hq // Hkv, D ** -0.5, float(cache.k_scale.max()))
+        del k, v
