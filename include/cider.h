@@ -695,9 +695,10 @@ cider_status_t cider_kv4_read(const cider_kv4_cache_t* cache, const int32_t* slo
  *   window     : 0, or the tokens j > p - window only.
  * A row that sees no token is zeros. Scores and the softmax's sums are fp32;
  * the weights are rounded to fp16 (11 bits) once they are multiplied by V's
- * scale, in units of a power of two above the largest finite scale of V (of
- * that group of dimensions) that rows of the sequence see: what is below 2^-25
- * of that scale is nothing. exp2 is the GPU's fp32 instruction.
+ * scale, in units of a power of two (2^-126 or more), of which the largest finite scale of V (of
+ * that group of dimensions) among the tokens of the sequence that any of its
+ * rows sees is at least 64: next to it, a weight (the row's largest being 1)
+ * times scale has a step of 2^-30, and below 2^-31 is nothing. exp2 is the GPU's fp32 instruction.
  * workspace: 16-byte aligned, at least cider_kv4_attention_workspace_size bytes
  * (capacity = max_pages * page_size; 0: none, NULL then). Its contents are
  * scratch; calls that share one must not overlap in time. The order of a row's

@@ -69,3 +69,49 @@ def test_long_sums(B, n, Hq, Hkv, L, D, G, dtype):
         picks = {(i, h) for i in at for h in range(0, Hq, max(1, Hq // 4))}
         check_rows(y, picks, q, k, v, Hq // Hkv, D ** -0.5, float(cache.k_scale.max()))
         del k, v
+
+
+# lengths, queries of each, query heads, key/value heads
+SPREAD = [([300, 90], [1, 1], 4, 2), ([500, 400], [3, 3], 4, 2), ([300], [300], 4, 2), ([700, 500], [90, 200], 4, 2),
+          ([4000], [1100], 2, 2), ([9000], [8800], 1, 1)]
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("D,gs", [(64, 0), (128, 32), (256, 128)])
+@pytest.mark.parametrize("lens,counts,Hq,Hkv", SPREAD)
+def test_a_large_scale_of_no_weight(lens, counts, Hq, Hkv, D, gs, dtype):
+    """A token in the middle of each sequence with keys opposed to every query, and a scale of V far above the others':
+    it has no weight, rows before it do not see it, and what is left of the others' weights is in units of its scale."""
+    from tests.test_gpu_kv4 import i32, setup
+    c, t, g = cider(), DT[dtype], gen(sum(lens) + D + gs)
+    page, G = 32, D // gs if gs else 1
+    for factor in (1e4, 1e5, 1e6):
+        q, cache, table, ends = setup(c, g, lens, counts, Hq, Hkv, D, gs, page, t)
+        q = (q.abs() + 0.25).to(t)
+        for b, L in enumerate(lens):
+            at = L - counts[b] // 2 - 2
+            p, o = int(table[b, at // page]), at % page
+            cache.k_codes[p, :, o] = 0x11                    # -7, of scores below -200
+            cache.k_scale[p, :, :, o] = 10.0
+            cache.v_scale[p, :, :, o] *= factor
+        y = c.cider_kv4_attention(q, cache, table, i32(lens), query_offsets=i32(ends))
+        err = weights = size = 0.0
+        for b, (L, n) in enumerate(zip(lens, counts)):
+            at = torch.arange(L, device="cuda")
+            at = at[at != L - n // 2 - 2]                    # the token itself adds nothing: 2^-200
+            k, v = ref.stored_rows(cache, table[b].long()[at // page] * page + at % page)
+            sv = cache.v_scale[table[b].long()[at // page], :, :, at % page].double().repeat_interleave(D // G, -1)
+            for i in {0, n // 3, n - 1}:
+                seen = at <= L - n + i
+                for h in range(Hq):
+                    u, q64 = h // (Hq // Hkv), q[ends[b] + i, h].double()
+                    want, spread, score = row(q64, k[seen, u], v[seen, u], D ** -0.5, 0.6)
+                    p = torch.softmax(D ** -0.5 * (k[seen, u] @ q64), 0)
+                    # half of the smallest step of fp16, 2^-25, in units of at most 1/64 of the largest scale; the
+                    # largest weight of a row is one at least
+                    lost = 2.0 ** -25 / 64 * 0.6 * factor * float(p.max()) * (v[seen, u] / sv[seen, u]).square().sum(0).sqrt()
+                    err += float((y[ends[b] + i, h].double() - want).square().sum())
+                    weights += float((spread * (2.0 ** -11 + 2 * score) + lost).square().sum())
+                    size += float(want.square().sum())
+        allowed = weights ** 0.5 + size ** 0.5 * (torch.finfo(t).eps / 2 + 2.0 ** -14)
+        assert err ** 0.5 <= allowed, (factor, err ** 0.5 / size ** 0.5, allowed / size ** 0.5)
