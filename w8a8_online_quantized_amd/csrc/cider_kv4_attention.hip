@@ -471,7 +471,13 @@ struct Rows {
       if (over[i] != kRaise) m[i] = kLeast;
       const float inv = l[i] == 0.0f ? 0.0f : 1.0f / l[i];
 #pragma unroll
-      for (int j = 0; j < kTiles; ++j) o[i][j] = o[i][j] * inv * ref[j / kPer];   // (ref * inv may be subnormal)
+      for (int g = 0; g < G; ++g) {
+        // (ref * inv may be subnormal; uniform, or the compiler keeps an array in LDS,
+        // whose addresses take the dispatch packet: 3 to 10 us of a launch)
+        const float unit = uniform(ref[g]);
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) o[i][g * kPer + j] = o[i][g * kPer + j] * inv * unit;
+      }
     }
   }
 
