@@ -115,3 +115,27 @@ def test_a_large_scale_of_no_weight(lens, counts, Hq, Hkv, D, gs, dtype):
                     size += float(want.square().sum())
         allowed = weights ** 0.5 + size ** 0.5 * (torch.finfo(t).eps / 2 + 2.0 ** -14)
         assert err ** 0.5 <= allowed, (factor, err ** 0.5 / size ** 0.5, allowed / size ** 0.5)
+
+
+@pytest.mark.parametrize("power", [-127, -119, -118, 118, 124])
+@pytest.mark.parametrize("n,L", [(1, 400), (90, 400), (40, 4000)])      # two joins of a few parts, one of many
+def test_scales_at_the_ends_of_the_type(n, L, power):
+    """Scales of V up to where bf16 results end, and down to where fp32 scales lose bits. (Sums of averages times their
+    weights would pass fp32's largest number before the results do.)"""
+    from tests.test_gpu_kv4 import i32, setup
+    c, g = cider(), gen(n)
+    q, cache, table, ends = setup(c, g, [L], [n], 4, 2, 128, 64, 16, torch.bfloat16)
+    cache.v_scale.mul_(2.0 ** power)
+    y = c.cider_kv4_attention(q, cache, table, i32([L]))
+    at = torch.arange(L, device="cuda")
+    k, v = ref.stored_rows(cache, table[0].long()[at // 16] * 16 + at % 16)
+    fin = torch.finfo(torch.bfloat16)
+    for i in {0, n // 2, n - 1}:
+        seen = L - n + i + 1
+        for h in range(4):
+            want, spread, score = row(q[i, h].double(), k[:seen, h // 2], v[:seen, h // 2], 128 ** -0.5, 0.6)
+            # (results and their roundings below the normal range: half a smallest step each, the fp32 ones' too)
+            allowed = spread.norm() * (2.0 ** -11 + 2 * score) + want.norm() * (fin.eps / 2 + 2.0 ** -14) + \
+                (fin.tiny * fin.eps + 2.0 ** -149) / 2 * 128 ** 0.5
+            assert float((y[i, h].double() - want).norm()) <= float(allowed), (i, h)
+            assert bool(y[i, h].isfinite().all())

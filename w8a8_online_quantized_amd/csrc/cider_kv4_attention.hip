@@ -834,21 +834,22 @@ __global__ void __launch_bounds__(kThreads, tokens_per_cu(D)) kv4_tokens(Kv4Atte
       float top = kLeast;
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) top = __builtin_fmaxf(top, shared.out.m[w][r]);
-      float sum = 0.0f, out[8];
+      float sum = 0.0f, f[kWaves], out[8];
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        f[w] = __builtin_amdgcn_exp2f(shared.out.m[w][r] - top) * shared.out.l[w][r];
+        sum += f[w];
+      }
+      // (parts of the sum first: averages times sums may pass fp32's largest where the result does not)
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
       for (int e = 0; e < 8; ++e) out[e] = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        const float f = __builtin_amdgcn_exp2f(shared.out.m[w][r] - top) * shared.out.l[w][r];
-        sum += f;
-        if (f != 0.0f) {
+      for (int w = 0; w < kWaves; ++w)
+        if (f[w] != 0.0f) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) out[e] = __builtin_fmaf(f, shared.out.o[w][r][8 * c + e], out[e]);
+          for (int e = 0; e < 8; ++e) out[e] = __builtin_fmaf(f[w] * inv, shared.out.o[w][r][8 * c + e], out[e]);
         }
-      }
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) out[e] *= inv;
       const int tok = (t.row0 + r) / t.heads;
       const int64_t to = (t.seq.q0 + tok) * a.q_heads + t.h * t.heads + (t.row0 + r) - tok * t.heads;
       if (whole) {
@@ -883,22 +884,39 @@ __global__ void __launch_bounds__(kThreads, tokens_per_cu(D)) kv4_tokens(Kv4Atte
 template <int D, bool BF>
 __global__ void __launch_bounds__(kThreads) kv4_join_pieces(Kv4AttentionArgs a, int blocks) {
   constexpr int kLanes = D / 8, kSlices = kThreads / kLanes;
-  __shared__ float slice_o[kSlices][D], slice_sum[kSlices], wave_top[kWaves];
+  __shared__ float slice_o[kSlices][D], wave_top[kWaves], wave_sum[kWaves];
   const int block = blockIdx.x, r = blockIdx.y;
   const Note note = reinterpret_cast<const Note*>(a.workspace)[block];
   if (note.parts == 0 || r >= note.rows) return;
   const int c = threadIdx.x % kLanes, slice = threadIdx.x / kLanes;
   auto piece = [&](int p) { return p == 0 ? 2 * (int64_t)block + 1 : 2 * (int64_t)(block + p); };
-  float top = kLeast;
-  for (int p = threadIdx.x; p < note.parts; p += kThreads)
-    top = __builtin_fmaxf(top, piece_ml(a, blocks, piece(p), r, D)->x);
+  // the maximum and the sum of all pieces, so that the averages enter with their parts of it
+  float top = kLeast, sum = 0.0f;
+  for (int p = threadIdx.x; p < note.parts; p += kThreads) {
+    const float2 ml = *piece_ml(a, blocks, piece(p), r, D);
+    const float to = __builtin_fmaxf(top, ml.x);
+    sum = sum * __builtin_amdgcn_exp2f(top - to) + ml.y * __builtin_amdgcn_exp2f(ml.x - to);
+    top = to;
+  }
+  float most = top;
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, off));
-  if ((threadIdx.x & 63) == 0) wave_top[threadIdx.x >> 6] = top;
+  for (int off = 32; off >= 1; off >>= 1) most = __builtin_fmaxf(most, __shfl_xor(most, off));
+  sum *= __builtin_amdgcn_exp2f(top - most);
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off);
+  if ((threadIdx.x & 63) == 0) {
+    wave_top[threadIdx.x >> 6] = most;
+    wave_sum[threadIdx.x >> 6] = sum;
+  }
   __syncthreads();
+  top = kLeast;
 #pragma unroll
   for (int w = 0; w < kWaves; ++w) top = __builtin_fmaxf(top, wave_top[w]);
-  float sum = 0.0f, out[8];
+  sum = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) sum += wave_sum[w] * __builtin_amdgcn_exp2f(wave_top[w] - top);
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  float out[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) out[e] = 0.0f;
 #pragma unroll 4
@@ -906,8 +924,7 @@ __global__ void __launch_bounds__(kThreads) kv4_join_pieces(Kv4AttentionArgs a, 
     const float2 ml = *piece_ml(a, blocks, piece(p), r, D);
     const float* po = piece_row(a, blocks, piece(p), r, D) + 8 * c;
     const f4 u = *reinterpret_cast<const f4*>(po), w = *reinterpret_cast<const f4*>(po + 4);
-    const float g = __builtin_amdgcn_exp2f(ml.x - top) * ml.y;
-    sum += g;
+    const float g = __builtin_amdgcn_exp2f(ml.x - top) * ml.y * inv;
     if (g != 0.0f) {                    // a piece without a visible token holds nothing
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -920,18 +937,13 @@ __global__ void __launch_bounds__(kThreads) kv4_join_pieces(Kv4AttentionArgs a, 
   if (slice > 0 && slice < used) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) slice_o[slice][8 * c + e] = out[e];
-    if (c == 0) slice_sum[slice] = sum;
   }
   __syncthreads();
   if (slice > 0) return;
   for (int s = 1; s < used; ++s) {
-    sum += slice_sum[s];
 #pragma unroll
     for (int e = 0; e < 8; ++e) out[e] += slice_o[s][8 * c + e];
   }
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) out[e] *= inv;
   const int hkv = a.cache.kv_heads, heads = a.q_heads / hkv, tok = (note.row0 + r) / heads;
   const int64_t to = ((int64_t)note.q0 + tok) * a.q_heads + note.h * heads + (note.row0 + r) - tok * heads;
   store16(static_cast<uint16_t*>(a.y) + to * D, c, pack8<BF>(out));
@@ -1169,19 +1181,22 @@ __global__ void __launch_bounds__(64 * W, rows_per_simd(D, W)) kv4_rows(Kv4Atten
 
 // ---- the join -------------------------------------------------------------------
 
-// An average in pieces: (m, l, o) each, joined in their order.
+// An average in pieces: (m, l, o) each, joined in their order. It stays an average (of what
+// was joined): a sum of l * o may pass fp32's largest where the result does not.
 struct Average {
   float top = kLeast, sum = 0.0f, out[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   __device__ __forceinline__ void add(float m, float l, const f4& u, const f4& w) {
     if (l == 0.0f) return;               // a piece without a visible token holds nothing
     const float to = __builtin_fmaxf(top, m);
-    const float f = __builtin_amdgcn_exp2f(top - to), g = __builtin_amdgcn_exp2f(m - to) * l;
+    const float f = __builtin_amdgcn_exp2f(top - to) * sum, g = __builtin_amdgcn_exp2f(m - to) * l;
     top = to;
-    sum = __builtin_fmaf(sum, f, g);
+    sum = f + g;
+    // (the GPU's reciprocal, one step off at most: 2^-18 over the 32 pieces of a chain)
+    const float inv = __builtin_amdgcn_rcpf(sum), old = f * inv, part = g * inv;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      out[e] = __builtin_fmaf(g, u[e], out[e] * f);
-      out[4 + e] = __builtin_fmaf(g, w[e], out[4 + e] * f);
+      out[e] = __builtin_fmaf(part, u[e], out[e] * old);
+      out[4 + e] = __builtin_fmaf(part, w[e], out[4 + e] * old);
     }
   }
 };
@@ -1238,19 +1253,21 @@ __global__ void __launch_bounds__(kThreads) kv4_join(Kv4AttentionArgs a, Plan pl
     }
     __syncthreads();
     if (slice > 0) return;
-    for (int s = 1; s < min(SLICES, sh.parts); ++s) {
-      // (a slice's sums are not averages yet: their weight is l / l)
-      const float to = __builtin_fmaxf(avg.top, slice_ml[s][0]);
-      const float f = __builtin_amdgcn_exp2f(avg.top - to), g = __builtin_amdgcn_exp2f(slice_ml[s][0] - to);
-      avg.top = to;
-      avg.sum = avg.sum * f + slice_ml[s][1] * g;
+    const int used = min(SLICES, sh.parts);
+    float top = avg.top;
+    for (int s = 1; s < used; ++s) top = __builtin_fmaxf(top, slice_ml[s][0]);
+    const float own = __builtin_amdgcn_exp2f(avg.top - top) * avg.sum;
+    float sum = own;
+    for (int s = 1; s < used; ++s) sum += __builtin_amdgcn_exp2f(slice_ml[s][0] - top) * slice_ml[s][1];
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) avg.out[e] = avg.out[e] * f + slice_o[s][8 * c + e] * g;
+    for (int e = 0; e < 8; ++e) avg.out[e] *= own * inv;
+    for (int s = 1; s < used; ++s) {
+      const float part = __builtin_amdgcn_exp2f(slice_ml[s][0] - top) * slice_ml[s][1] * inv;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) avg.out[e] = __builtin_fmaf(part, slice_o[s][8 * c + e], avg.out[e]);
     }
   }
-  const float inv = avg.sum == 0.0f ? 0.0f : 1.0f / avg.sum;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) avg.out[e] *= inv;
   store16(static_cast<uint16_t*>(a.y) + (int64_t)row * D, c, pack8<BF>(avg.out));
 }
 
