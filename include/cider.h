@@ -685,10 +685,11 @@ cider_status_t cider_kv4_read(const cider_kv4_cache_t* cache, const int32_t* slo
  *                tokens of a page outside [0, n_pages) are not seen.
  *   query_offsets : int32 [B + 1] on the device: sequence b has the query rows
  *                query_offsets[b] .. query_offsets[b+1] - 1, ascending from 0 to
- *                at most T (offsets that do not ascend are clamped to it, and
- *                rows that come in two sequences are then written by either);
- *                or NULL: T / B rows each, T a multiple of B. Rows of no
- *                sequence are left as they were.
+ *                at most T; or NULL: T / B rows each, T a multiple of B. Rows of
+ *                no sequence are left as they were. Offsets that lie outside
+ *                0 .. T are clamped to it; where they do not ascend, the values
+ *                of y are undefined, and nothing but y and the workspace is
+ *                written.
  *   y          : [T, q_heads, head_dim], contiguous; must not overlap q.
  *   causal     : 1: query i of n is at position p = length - n + i and sees the
  *                tokens j <= p. 0: it sees all tokens of its sequence.
