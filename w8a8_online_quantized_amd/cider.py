@@ -885,8 +885,11 @@ class KV4Cache(typing.NamedTuple):
 
 def kv4_cache(n_pages: int, kv_heads: int, page_size: int, head_dim: int, group_size: int = 0, device=None) -> KV4Cache:
     """An empty KV4Cache (codes 0, scales 0) on the current device. group_size 0
-    gives one scale per token and head, 32 or more one per group of dimensions."""
+    gives one scale per token and head, 32 or more one per group of dimensions
+    (head_dim, or a half or a quarter of it)."""
     import torch
+    if group_size and (group_size < 32 or group_size not in (head_dim, head_dim / 2, head_dim / 4)):
+        raise ValueError(f"group_size must be 0, or head_dim, head_dim / 2 or head_dim / 4 and at least 32, got {group_size}")
     G = head_dim // group_size if group_size else 1
     device = device or torch.device("cuda", torch.cuda.current_device())
     codes, scale = (n_pages, kv_heads, page_size, head_dim // 2), (n_pages, kv_heads, G, page_size)
