@@ -960,6 +960,20 @@ def _need_rows(dev, t, dtype, shape, name):
     return (row if T > 1 else H * D), head
 
 
+def _refused(fn, status, cache=None, **tensors):
+    """Raise for a call that returned a status, and say which tensors start at
+    no multiple of 16 bytes, as slices like slots[1:] may: of all that these
+    calls refuse, what a tensor's type and shape do not show."""
+    if status == CIDER_ERROR_INVALID_VALUE:
+        if cache is not None:
+            tensors.update(cache._asdict() if isinstance(cache, KV4Cache) else zip(KV4Cache._fields, cache))
+        off = [name for name, t in tensors.items() if t is not None and t.data_ptr() % 16]
+        if off:
+            raise CiderError(fn, status, f"{status_string(status)}: {', '.join(off)} must start at a multiple of 16 bytes "
+                                         "(a slice's copy does)")
+    _check(fn, status)
+
+
 def _cache_args(dev, cache):
     """The values of cider_kv4_cache_t."""
     import torch
@@ -1006,7 +1020,7 @@ def cider_rope(x, positions, inv_freq, interleaved: bool = False, scale: float =
                       1 if interleaved else 0, scale)
     st = lib().cider_rope(args, _raw_stream(stream, dev))
     if st:
-        _check("cider_rope", st)
+        _refused("cider_rope", st, x=x, positions=positions, inv_freq=inv_freq, y=y)
     return y
 
 
@@ -1056,7 +1070,8 @@ def cider_kv4_append(cache, k, v, slots, q=None, positions=None, inv_freq=None, 
                         kh, vr, vh, our, ouh, _fp_code(k, "k"), Hq, rd, 1 if interleaved else 0, rope_scale, eps)
     st = lib().cider_kv4_append(args, _raw_stream(stream, dev))
     if st:
-        _check("cider_kv4_append", st)
+        _refused("cider_kv4_append", st, cache, k=k, v=v, slots=slots, q=q, positions=positions, inv_freq=inv_freq,
+                 q_norm=q_norm, k_norm=k_norm, q_out=q_out)
     return q_out
 
 
@@ -1081,7 +1096,7 @@ def cider_kv4_read(cache, slots, k=None, v=None, stream=None, out_dtype=None):
     st = lib().cider_kv4_read(_pack_cache(*arrays), slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), _fp_code(k, "k"),
                               _raw_stream(stream, dev))
     if st:
-        _check("cider_kv4_read", st)
+        _refused("cider_kv4_read", st, cache, slots=slots, k=k, v=v)
     return k, v
 
 
@@ -1144,7 +1159,8 @@ def cider_kv4_attention(q, cache, page_table, lengths, query_offsets=None, causa
                            D ** -0.5 if softmax_scale is None else softmax_scale)
     st = lib().cider_kv4_attention(args, _raw_stream(stream, dev))
     if st:
-        _check("cider_kv4_attention", st)
+        _refused("cider_kv4_attention", st, cache, q=q, page_table=page_table, lengths=lengths, query_offsets=query_offsets,
+                 y=y, workspace=workspace)
     return y
 
 
