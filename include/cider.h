@@ -578,7 +578,7 @@ cider_status_t cider_dequant_act(const int8_t* x_q, const float* x_scale, int64_
  * CIDER_ROPE_MAX_HEAD_DIM; rotary_dim even, at most head_dim and
  * CIDER_ROPE_MAX_ROTARY_DIM. Head sizes and strides that are not multiples of
  * 8, and half layouts whose rotary_dim is not one of 16, take a slower path
- * with the same results. (T, heads, head_dim) whose grid would take 2^31 GPU
+ * with the same results (x and y start at multiples of 16 bytes all the same). (T, heads, head_dim) whose grid would take 2^31 GPU
  * threads return CIDER_ERROR_INVALID_VALUE. */
 typedef struct {
   const void* x;
@@ -634,7 +634,8 @@ typedef struct {
  * stored; its q is still written. The slots of a call must differ: tokens that
  * share one leave codes and scales of either in it. A group of k or v that
  * holds an infinity or a NaN is stored with the scale NaN and codes 0, so the
- * rows that attend to it become NaN and no others.
+ * rows that attend to it become NaN and no others. A norm of a head that is not
+ * finite or whose squares overflow fp32 makes the whole head NaN.
  *   q, q_out [T, q_heads, head_dim] (both or neither; q_out may be q), k, v [T,
  *   kv_heads, head_dim], fp16 or bf16 (dtype), strides in elements, multiples
  *   of 8; q_norm, k_norm [head_dim] or NULL; positions int32 [T] and inv_freq
