@@ -35,16 +35,17 @@
 // Two kernels. kv4_tokens is for few rows (a decode step): the four waves of a
 // workgroup share a tile of 16 rows and take the tokens in turn, codes from
 // global memory straight to registers; what bounds it is the stream of the
-// codes. kv4_rows is for many: each wave has 32 rows, and the workgroup
+// codes. kv4_rows is for many: each wave has 16 or 32 rows, and the workgroup
 // unpacks a stage of tokens once, into LDS, in the operands' own order. In both
 // the tokens are also split over workgroups when there are few tiles; their
 // partial results are joined by a second launch.
 //
-// Measured (heads of 128, bf16): 64 requests of up to 8192 tokens 86 us for 333 MB
-// = 3.9 TB/s (the loads alone take 71, the read rate would allow 54); a prompt of
-// 8192 tokens, 16 heads, 325 us = 850 TFLOP/s, and 512 queries on 32768 tokens 175
-// us = 780 TFLOP/s, where a large matrix product reaches 1190: the softmax's and the
-// unpacking's vector instructions share the SIMDs with the matrix core.
+// Measured (heads of 128, bf16): 64 requests of up to 8192 tokens 88 us for 333 MB
+// = 3.8 TB/s (the loads alone take 71, the read rate would allow 54); a prompt of
+// 8192 tokens, 16 heads, 319 us = 860 TFLOP/s, and 512 queries on 32768 tokens 175
+// us = 780 TFLOP/s, where a large matrix product reaches 1190: products, softmax and
+// products follow each other in a wave, and the waves of a SIMD start a stage together,
+// so the matrix core and the vector unit mostly take turns.
 #include "cider_internal.h"
 #include "cider_quant_rule.h"
 #include "cider_rows.h"
@@ -59,8 +60,8 @@ constexpr int kWaves = kThreads / 64;
 constexpr int kTokens = 32;            // of one step of products
 // Tiles of 16 rows of a wave of kv4_rows (W waves): what 256 registers hold without
 // spills; heads of 64 in two groups one in workgroups of four waves, of which a CU
-// then holds three (five prompts of about 1000 tokens 69 us, with two tiles 79; two
-// in workgroups of eight: 512 queries on 32768 tokens 175 us, with one tile 231).
+// then holds three (five prompts of about 1000 tokens 66 us, with two tiles 87; two
+// in workgroups of eight: 512 queries on 32768 tokens 172 us, with one tile 226).
 constexpr int row_tiles(int D, int G, int W) { return D == 256 || (D / G == 32 && !(D == 64 && W == 8)) ? 1 : 2; }
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLeast = -3.402823466e38f;
@@ -538,8 +539,8 @@ struct Raw {
 };
 
 // Workgroups of kv4_tokens that a CU holds at once: two waves per SIMD, without
-// spills (three: the decode batch below 117 us instead of 86), one for D = 256, which
-// needs more than 256 registers (24 requests of 5 queries in a window of 3000: two 55
+// spills (three: the decode batch below 107 us instead of 89), one for D = 256, which
+// needs more than 256 registers (24 requests of 5 queries in a window of 3000: two 56
 // us with spills, one 35).
 constexpr int tokens_per_cu(int D) { return D == 256 ? 1 : 2; }
 
@@ -765,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, tokens_per_cu(D)) kv4_tokens(Kv4Atte
     Raw<D, G> raw;
   };
   // Two steps in registers, one on its way while the other is worked on (64 requests
-  // of up to 8192 tokens 86 us; three steps 90, four 92). The loads are unconditional
+  // of up to 8192 tokens 89 us; three steps 93, four 94). The loads are unconditional
   // (past the end, of the last codes again): behind a branch the wait for one step's
   // would be one for all in flight.
   constexpr int kRing = 2;
@@ -951,14 +952,14 @@ __global__ void __launch_bounds__(kThreads) kv4_join_pieces(Kv4AttentionArgs a, 
 
 // ---- many rows ------------------------------------------------------------------
 
-// Workgroups of W waves, 4 (two per CU) or 8 (one, with twice the rows and tokens
-// per stage: a wave then unpacks half as much per token).
+// Workgroups of W waves, 4 (two per CU, of heads of 64 three) or 8 (one, with twice the
+// rows and tokens per stage: a wave then unpacks half as much per token).
 // Tokens of a stage: two stages of operands are 64 KB (128 KB), of D = 64 half that.
 constexpr int stage_tokens(int D, int W) { return (D == 256 ? 32 : 64) * W / 4; }
 
 // Waves per SIMD: two, of heads of 64 in workgroups of four waves three (one group,
-// five prompts of about 1000 tokens: 57 us with three, 63 with two; two groups with
-// four, which takes spills, are no faster than with three).
+// five prompts of about 1000 tokens: 57 us with three, 62 with two; two groups are no
+// faster with four than with three, 67 us).
 constexpr int rows_per_simd(int D, int W) { return D == 64 && W == 4 ? 3 : 2; }
 
 template <int D, int G, bool BF, int W>
@@ -1275,19 +1276,23 @@ __global__ void __launch_bounds__(kThreads) kv4_join(Kv4AttentionArgs a, Plan pl
 
 // Up to two tiles of 16 rows per sequence and key/value head. With a threshold of 16,
 // 32 and 64 (us, 8192 tokens, heads of 128, 8 per key/value head, 2 of those): sixteen
-// sequences of 24 rows 35, 31, 31; two of 64 rows 23, 23, 30; sixteen of 64 rows 44,
-// 44, 39. Past 32 it depends on how many sequences there are, and few would lose more.
+// sequences of 24 rows 35, 32, 32; two of 64 rows 23, 23, 31; sixteen of 64 rows 44,
+// 44, 42. Past 32 it depends on how many sequences there are, and few would lose more.
+// The rule takes the average, since the host does not know the offsets: 63 single tokens
+// on 8192 and 512 queries on 8192 in one call 203 us (two calls 132 + 73), on 32768 432
+// (132 + 181), 2048 queries on 8192 537 (132 + 168), as a long sequence's tiles of 16 rows
+// each unpack its tokens again.
 bool few_rows(int64_t T, int64_t B, int heads) { return T * heads <= 32 * B; }
 
 // kv4_rows. Whole prompts (no more than twice as many tokens as queries) have tiles of
 // all lengths, which are done as workgroups come free; other queries see about as many
 // tokens each. Eight waves per workgroup pay from 8192 rows per sequence and key/value
 // head in the first case (heads of 128, two query heads each; us with 8, 4 waves: 8192
-// tokens 324, 358; 4096 tokens 122, 124; 2048 tokens 69, 67; five of about 1000 tokens,
-// three heads of 64: 81, 65), from 1024 in the second (512 queries on 8192 tokens 68, 71;
-// on 32768 175, 190). Tokens are split until there are as many parts as workgroups are
-// resident, for whole prompts twice as many (2048 tokens: 2 parts 119, 4 parts 67; 512
-// queries on 32768 tokens: 8 parts 190, 16 parts 220).
+// tokens 319, 356; 4096 tokens 119, 126; 2048 tokens 67, 66; five of about 1000 tokens,
+// three heads of 64: 82, 66), from 1024 in the second (512 queries on 8192 tokens 67, 71;
+// on 32768 175, 191). Tokens are split until there are as many parts as workgroups are
+// resident, for whole prompts twice as many (4096 tokens: 1 part 152, 2 parts 119; 2048
+// tokens: 2 parts 59, 4 parts 66; 512 queries on 32768 tokens: 8 parts 175, 16 parts 200).
 Plan plan_of(int64_t T, int64_t B, int q_heads, int kv_heads, int head_dim, int groups, int64_t capacity, bool ragged) {
   const int heads = q_heads / kv_heads;
   const int64_t rows = T * heads;

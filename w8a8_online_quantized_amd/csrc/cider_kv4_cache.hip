@@ -8,10 +8,11 @@
 //   kv4_read_rows    the slots' codes times their scales -> 16-bit rows
 //
 // k is rounded to its 16-bit type before it is quantized, so that the codes are
-// those of a rotated k that was stored in between. HBM-bound: every row is read
-// once, q written once, and the codes are a quarter of what was read. (16384 tokens,
-// 16 heads of q, 8 of k and v of 128, norms and rotation: 54.7 us for 220 MB = 4.0
-// TB/s, the vector units busy throughout; read back 22.2 us for 86 MB.)
+// those of a rotated k that was stored in between. Every row is read once, q
+// written once, and the codes are a quarter of what was read. (16384 tokens, 16 heads
+// of q, 8 of k and v of 128, norms and rotation: 54.7 us for 220 MB = 4.0 TB/s where a
+// copy reaches 5.2: the vector units, busy throughout, bound it with HBM close behind;
+// read back 22.2 us for 86 MB, bound by its 64-byte pieces of rows.)
 //
 // D / 8 lanes hold one head, eight dimensions each; the sums of a norm and the
 // maxima of the groups stay in those lanes.

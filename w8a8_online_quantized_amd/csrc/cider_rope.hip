@@ -4,8 +4,8 @@
 // HBM-bound: 2 bytes in and 2 out per element (16384 tokens of 24 heads of 128: 201
 // MB in 39.4 us = 5.1 TB/s, a copy's rate). One workgroup per token (and
 // slice of its heads): its threads first form the token's rotary_dim / 2
-// cosines and sines into LDS, shared by all heads, while the rows' loads are on
-// their way. A thread then owns both ends of the pairs it turns, so y may be x.
+// cosines and sines into LDS, shared by all heads; other workgroups' rows are on
+// their way meanwhile. A thread then owns both ends of the pairs it turns, so y may be x.
 #include "cider_internal.h"
 #include "cider_quant_rule.h"
 #include "cider_rope.h"
