@@ -139,3 +139,24 @@ def test_scales_at_the_ends_of_the_type(n, L, power):
                 (fin.tiny * fin.eps + 2.0 ** -149) / 2 * 128 ** 0.5
             assert float((y[i, h].double() - want).norm()) <= float(allowed), (i, h)
             assert bool(y[i, h].isfinite().all())
+
+
+@pytest.mark.parametrize("D,G", [(64, 2), (128, 1), (256, 2)])
+@pytest.mark.parametrize("B,n,Hq,Hkv,L", [(1, 2048, 32, 4, 131001), (64, 1, 8, 8, 131001), (1, 70, 4, 1, 131001),
+                                          (1, 1, 16, 8, 131001), (1, 1000, 2, 1, 131001)])
+def test_no_part_of_a_long_range_is_lost(B, n, Hq, Hkv, L, D, G):
+    """Equal weights over codes of V that rise from 0 to 6: without the first or the last page of 1024 the average would be
+    off by 2^-10 of itself, without a part of a join by far more, and the bound is 2^-10.8."""
+    c, g = cider(), gen(L + D + n)
+    cache = long_cache(g, c, L, Hkv, D, G, 0.0)
+    pages = cache.k_codes.shape[0]
+    rise = torch.linspace(0.0, 6.0, pages, device="cuda").view(-1, 1, 1, 1) + 1.5 * torch.rand(pages, Hkv, 128, D, generator=g, device="cuda") - 0.75
+    cache.v_codes.copy_(ref.pack(rise.round_().clamp_(-7, 7)))
+    cache.v_scale.fill_(0.4)
+    table = torch.arange(pages, device="cuda", dtype=torch.int32).repeat(B, 1)
+    q = torch.zeros(B * n, Hq, D, dtype=torch.float16, device="cuda")
+    y = c.cider_kv4_attention(q, cache, table, torch.full((B,), L, dtype=torch.int32, device="cuda"), causal=False)
+    _, v = ref.stored_rows(cache, torch.arange(L, device="cuda"))
+    want = v.mean(0).repeat_interleave(Hq // Hkv, 0)
+    off = (y.double() - want).flatten(1).norm(dim=1) / want.norm()
+    assert float(off.max()) <= 2.0 ** -11 + 2.0 ** -14, float(off.max())
